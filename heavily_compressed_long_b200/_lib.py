@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libhcl.so")
 
 HCL_OK, HCL_ERR_INVALID_ARG, HCL_ERR_UNSUPPORTED, HCL_ERR_CUDA = 0, 1, 2, 4
-HCL_ERR_TIMEOUT, HCL_ERR_DEVICE_FAULT = 8, 16
+HCL_ERR_TIMEOUT, HCL_ERR_DEVICE_FAULT, HCL_ERR_NO_PAGES = 8, 16, 32
 HCL_BF16, HCL_FP32, HCL_FP8SPLIT, HCL_MXFP4 = 0, 1, 2, 3
 
 P = ctypes.c_void_p
@@ -25,6 +25,14 @@ class hcl_kv_t(ctypes.Structure):
 
 
 KVP = ctypes.POINTER(hcl_kv_t)
+
+
+class hcl_paged_kv_t(ctypes.Structure):
+    _fields_ = [("page", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("k", P), ("v", P), ("k_scale", P), ("v_scale", P)]
+
+
+PKVP = ctypes.POINTER(hcl_paged_kv_t)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -53,6 +61,10 @@ SIGNATURES = {
     "hcl_cp_candidates": (I, [P, I, P, I, I, I, I, P, P, P, P]),
     "hcl_cp_own": (I, [P, P, I, I, I, I, I, P, P, P]),
     "hcl_lse_merge": (I, [P, P, I, I64, I, I, P, P, P, P]),
+    "hcl_page_plan": (I, [P, P, I, I, P, P, I, P, I, P, I, P, P, P, P, P]),
+    "hcl_paged_write": (I, [P, I64, P, I64, P, I, PKVP, P, P]),
+    "hcl_paged_attn_workspace_bytes": (SZ, [I, I, I, I]),
+    "hcl_paged_attn": (I, [P, I64, I, I, P, P, I, PKVP, P, I, P, I, I, I, F, P, P, P, P, SZ, P, P]),
     "hcl_selftest_bounded_wait": (I, [P, I, P]),
 }
 

@@ -570,6 +570,105 @@ hcl_status_t hcl_lse_merge(const void* o_parts, const float* lse_parts, int G, i
                           as_stream(stream));
 }
 
+// ---- paged 8-bit cache -------------------------------------------------------------------
+
+static bool page_size_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+static hcl_status_t check_paged(const hcl_paged_kv_t* kv) {
+  HCL_REQUIRE(kv != nullptr, "kv must be given");
+  if (!page_size_ok(kv->page))
+    return fail(HCL_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", kv->page);
+  if (kv->d != 64 && kv->d != 128)
+    return fail(HCL_ERR_UNSUPPORTED, "paged cache: d must be 64 or 128 (got %d)", kv->d);
+  HCL_REQUIRE(kv->n_pages >= 1 && kv->Hkv >= 1, "n_pages and Hkv must be positive");
+  HCL_REQUIRE((long long)kv->n_pages * kv->page * kv->Hkv < (1ll << 31),
+              "n_pages * page * Hkv must be below 2^31");
+  HCL_REQUIRE(kv->k && kv->k_scale, "k and k_scale must be given");
+  HCL_REQUIRE((kv->v != nullptr) == (kv->v_scale != nullptr), "v and v_scale go together");
+  HCL_REQUIRE((reinterpret_cast<uintptr_t>(kv->k) & 127) == 0 &&
+                  (reinterpret_cast<uintptr_t>(kv->v) & 127) == 0,
+              "k and v must be 128-byte aligned");
+  HCL_REQUIRE((reinterpret_cast<uintptr_t>(kv->k_scale) & 3) == 0 &&
+                  (reinterpret_cast<uintptr_t>(kv->v_scale) & 3) == 0,
+              "scales must be 4-byte aligned");
+  return HCL_OK;
+}
+
+hcl_status_t hcl_page_plan(const int32_t* keep, const int32_t* new_len, int B, int page,
+                           int32_t* seq_len, int32_t* table, int max_pages, int32_t* free_list,
+                           int n_pages, int32_t* n_free, int T, int32_t* cu_new, int32_t* pos,
+                           int32_t* slot, int32_t* status, void* stream) {
+  if (!page_size_ok(page))
+    return fail(HCL_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", page);
+  HCL_REQUIRE(B >= 0 && T >= 0 && n_pages >= 0, "negative size");
+  if (B > 8192) return fail(HCL_ERR_UNSUPPORTED, "page plan: B must be <= 8192 (got %d)", B);
+  HCL_REQUIRE(T <= (1 << 29), "T must be <= 2^29");
+  HCL_REQUIRE(max_pages >= 1 || B == 0, "max_pages must be positive");
+  HCL_REQUIRE((long long)B * max_pages < (1ll << 31), "B * max_pages must be below 2^31");
+  HCL_REQUIRE((long long)n_pages * page < (1ll << 31), "n_pages * page must be below 2^31");
+  HCL_REQUIRE((long long)max_pages * page < (1ll << 31), "max_pages * page must be below 2^31");
+  HCL_REQUIRE(cu_new != nullptr, "cu_new must be given");
+  HCL_REQUIRE(B == 0 || (keep && new_len && seq_len && table), "NULL pointer");
+  HCL_REQUIRE(n_free && (free_list || n_pages == 0), "n_free and free_list must be given");
+  HCL_REQUIRE(T == 0 || (pos && slot), "pos and slot must be given");
+  PagePlanArgs a{keep, new_len, B, page, seq_len, table, max_pages, free_list, n_pages, n_free,
+                 T, cu_new, pos, slot, status};
+  return launch_page_plan(a, as_stream(stream));
+}
+
+hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const void* v_new,
+                             int64_t v_stride, const int32_t* slot, int T,
+                             const hcl_paged_kv_t* kv, int32_t* status, void* stream) {
+  HCL_REQUIRE(T >= 0, "negative size");
+  hcl_status_t e = check_paged(kv);
+  if (e != HCL_OK) return e;
+  if (T == 0) return HCL_OK;
+  HCL_REQUIRE(k_new && slot, "NULL pointer");
+  HCL_REQUIRE((v_new != nullptr) == (kv->v != nullptr), "v_new must be given exactly when kv has v");
+  const int64_t row = (int64_t)kv->Hkv * kv->d;
+  HCL_REQUIRE(k_stride >= row && k_stride % 8 == 0, "k_stride must be >= Hkv * d and a multiple of 8");
+  HCL_REQUIRE(!v_new || (v_stride >= row && v_stride % 8 == 0),
+              "v_stride must be >= Hkv * d and a multiple of 8");
+  HCL_REQUIRE(aligned16(k_new) && aligned16(v_new), "k_new and v_new must be 16-byte aligned");
+  PagedWriteArgs a{{k_new, v_new}, {k_stride, v_stride}, slot, T, *kv, status};
+  return launch_paged_write(a, as_stream(stream));
+}
+
+size_t hcl_paged_attn_workspace_bytes(int T, int H, int Hkv, int d) {
+  return hcl::paged_attn_workspace_bytes(T, H, Hkv, d);
+}
+
+hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int H, const int32_t* cu_q,
+                            const int32_t* q_start, int B, const hcl_paged_kv_t* kv,
+                            const int32_t* table, int max_pages, const int32_t* kv_len, int max_q,
+                            int m, int W, float scale, const float* sink, void* out, float* lse,
+                            void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  HCL_REQUIRE(T >= 0 && B >= 0, "negative size");
+  hcl_status_t e = check_paged(kv);
+  if (e != HCL_OK) return e;
+  HCL_REQUIRE(H >= 1 && H % kv->Hkv == 0, "H must be a positive multiple of Hkv");
+  if (H / kv->Hkv > 128) return fail(HCL_ERR_UNSUPPORTED, "paged attention: H / Hkv must be <= 128");
+  if (B > 8192) return fail(HCL_ERR_UNSUPPORTED, "paged attention: B must be <= 8192 (got %d)", B);
+  HCL_REQUIRE(m >= 1 && W >= 0, "m must be positive, W not negative");
+  HCL_REQUIRE(W == 0 || m == 1, "a window needs m == 1");
+  HCL_REQUIRE(scale > 0.f && scale < 1e30f, "scale must be a positive number");
+  HCL_REQUIRE(max_q >= 0, "max_q must not be negative");
+  HCL_REQUIRE((long long)T * H < (1ll << 31), "T * H must be below 2^31");
+  if (T == 0 || B == 0) return HCL_OK;
+  HCL_REQUIRE(q && cu_q && q_start && table && kv_len && out, "NULL pointer");
+  HCL_REQUIRE(max_pages >= 1 && (long long)max_pages * kv->page < (1ll << 31),
+              "max_pages must be positive, max_pages * page below 2^31");
+  HCL_REQUIRE(q_stride >= (int64_t)H * kv->d && q_stride % 8 == 0,
+              "q_stride must be >= H * d and a multiple of 8");
+  HCL_REQUIRE(aligned16(q) && aligned16(out), "q and out must be 16-byte aligned");
+  const size_t need = hcl::paged_attn_workspace_bytes(T, H, kv->Hkv, kv->d);
+  HCL_REQUIRE(ws_bytes >= need && (need == 0 || (ws && aligned16(ws))),
+              "workspace too small or not 16-byte aligned: need %zu bytes", need);
+  PagedAttnArgs a{q, q_stride, T, H, cu_q, q_start, B, *kv, table, max_pages, kv_len, max_q, m, W,
+                  scale, sink, out, lse, status};
+  return launch_paged_attn(a, ws, as_stream(stream));
+}
+
 hcl_status_t hcl_selftest_bounded_wait(int32_t* status, int limit_us, void* stream) {
   HCL_REQUIRE(status != nullptr, "status must be given");
   HCL_REQUIRE(limit_us >= 1 && limit_us <= 10 * 1000 * 1000, "limit_us must be in [1, 1e7]");

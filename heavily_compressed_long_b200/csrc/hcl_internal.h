@@ -195,6 +195,56 @@ hcl_status_t launch_lse_merge(const void* o, const float* lse, int G, long long 
 constexpr size_t NOALLOC_SCRATCH_BYTES = size_t(16) << 20;
 hcl_status_t noalloc_scratch(void** ptr);
 
+// Paged 8-bit cache (page.cu: plan and write; paged_attn.cu).
+struct PagePlanArgs {
+  const int32_t* keep;
+  const int32_t* new_len;
+  int B, page;
+  int32_t* seq_len;
+  int32_t* table;
+  int max_pages;
+  int32_t* free_list;
+  int n_pages;
+  int32_t* n_free;
+  int T;
+  int32_t* cu_new;
+  int32_t* pos;
+  int32_t* slot;
+  int32_t* status;
+};
+hcl_status_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st);
+
+struct PagedWriteArgs {
+  const void* src[2];   // k_new, v_new (or null)
+  int64_t stride[2];    // elements per token
+  const int32_t* slot;
+  int T;
+  hcl_paged_kv_t kv;
+  int32_t* status;
+};
+hcl_status_t launch_paged_write(const PagedWriteArgs& a, cudaStream_t st);
+
+struct PagedAttnArgs {
+  const void* q;
+  int64_t q_stride;
+  int T, H;
+  const int32_t* cu_q;
+  const int32_t* q_start;
+  int B;
+  hcl_paged_kv_t kv;
+  const int32_t* table;
+  int max_pages;
+  const int32_t* kv_len;
+  int max_q, m, W;
+  float scale;
+  const float* sink;
+  void* out;
+  float* lse;
+  int32_t* status;
+};
+size_t paged_attn_workspace_bytes(int T, int H, int Hkv, int d);
+hcl_status_t launch_paged_attn(const PagedAttnArgs& a, void* ws, cudaStream_t st);
+
 hcl_status_t launch_selftest_wait(int32_t* status, int limit_us, cudaStream_t st);
 
 }  // namespace hcl

@@ -59,7 +59,8 @@ typedef enum {
   HCL_ERR_UNSUPPORTED = 2,   /* a valid combination this build does not implement */
   HCL_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed */
   HCL_ERR_TIMEOUT = 8,       /* (device status bit) a bounded wait ran out */
-  HCL_ERR_DEVICE_FAULT = 16  /* (device status bit) an out-of-range index was skipped */
+  HCL_ERR_DEVICE_FAULT = 16, /* (device status bit) an out-of-range index was skipped */
+  HCL_ERR_NO_PAGES = 32      /* (device status bit) a request did not get its cache pages */
 } hcl_status_t;
 
 typedef enum {
@@ -323,6 +324,111 @@ HCL_API hcl_status_t hcl_cp_own(const int32_t* pos, const int32_t* gathered_idx,
 HCL_API hcl_status_t hcl_lse_merge(const void* o_parts, const float* lse_parts, int G, int64_t rows,
                                    int d, int H, const float* sink, void* out, float* lse_out,
                                    void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Paged 8-bit KV cache for ragged batches [Yanbaoke §5 KV cache management names a paged,
+ * heterogeneous cache only; the layout and the numerics are this library's own].
+ * A page holds `page` consecutive rows (raw tokens, or compressed entries) of one request as
+ * E4M3 codes with one fp32 scale per page and KV head: row r of KV head g in page n is
+ *     k_scale[n, g] * k[n, g, r, :]           (codes: e4m3 [n_pages, Hkv, page, d])
+ * and likewise v.  v == NULL (with v_scale == NULL): each row is both key and value, as in the
+ * other stores.  Request b's row t lives in page table[b, t / page] at offset t % page, its
+ * "slot" is table[b, t / page] * page + t % page.
+ * Supported: page 16, 32, 64 or 128; d 64 or 128; Hkv >= 1; n_pages * page < 2^31 and
+ * n_pages * Hkv * page < 2^31.  Code planes 128-byte aligned.
+ */
+typedef struct {
+  int32_t page;
+  int32_t n_pages;
+  int32_t Hkv;
+  int32_t d;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} hcl_paged_kv_t;
+
+/*
+ * hcl_page_plan -- block tables and slot maps for one step, from the requests' lengths.
+ * Request b holds seq_len[b] rows; keep[b] of them stay (keep == seq_len: plain growth; less:
+ * rejected draft tokens are dropped; 0: the row of the table serves a new request) and
+ * new_len[b] rows are appended.  With up(x) = ceil(x / page):
+ *   1. pages up(keep) .. up(seq_len) - 1 of every request go back to the free list, which is a
+ *      stack: free_list[0 .. n_free - 1] are free, the last one is taken first.  They are pushed
+ *      so that the first request's first page ends on top.
+ *   2. request after request takes up(keep + new_len) - up(keep) pages.
+ *   3. cu_new[b] = new_len[0] + .. + new_len[b - 1] (cu_new[B]: all);  for the i-th new row of
+ *      request b, t = cu_new[b] + i:  pos[t] = keep[b] + i,  slot[t] = its slot.  Rows
+ *      cu_new[B] <= t < T get pos = slot = -1 (T: the capacity of pos and slot).
+ *   4. seq_len[b] = keep[b] + new_len[b], *n_free and table are updated; table entries of
+ *      released pages that are not taken again become -1.
+ * Planning the same step again (the same keep and new_len) leaves the same tables.
+ * keep may be seq_len itself.  A request that does not get its rows -- the free list is too
+ * short for it and those before it, its length exceeds max_pages * page, or its rows end
+ * beyond T -- takes no page, keeps keep[b] rows and gets slot = -1: HCL_ERR_NO_PAGES.  Lengths
+ * out of range (keep > seq_len, negative values) are clamped: HCL_ERR_DEVICE_FAULT.  (cu_new
+ * counts the given new_len in every case, but is never above T.)
+ *   keep, new_len int32 [B]; seq_len int32 [B], table int32 [B, max_pages], free_list int32
+ *   [n_pages], n_free int32: updated in place; cu_new int32 [B + 1], pos, slot int32 [T].
+ * Supported: B <= 8192, T <= 2^29, page 16, 32, 64 or 128, B * max_pages < 2^31,
+ * n_pages * page < 2^31.
+ */
+HCL_API hcl_status_t hcl_page_plan(const int32_t* keep, const int32_t* new_len, int B, int page,
+                                   int32_t* seq_len, int32_t* table, int max_pages,
+                                   int32_t* free_list, int n_pages, int32_t* n_free, int T,
+                                   int32_t* cu_new, int32_t* pos, int32_t* slot, int32_t* status,
+                                   void* stream);
+
+/*
+ * hcl_paged_write -- quantises new rows into the pages of `kv`.
+ *   k_new, v_new bf16 [T, Hkv, d], token stride k_stride / v_stride elements (>= Hkv * d, a
+ *   multiple of 8; v_new NULL exactly when kv->v is); slot int32 [T], < 0: the row is skipped.
+ * Scales are powers of two, so that raising one moves only exponents: with amax the largest
+ * finite |x| of the call's rows of one page and KV head, the page's scale becomes the least
+ * power of two s >= 2^-126 with amax / s <= 448 -- and, unless the call writes the page's first
+ * row, at least the scale the page had.  Codes are E4M3 round-to-nearest-even of x / s,
+ * saturating (infinities too); NaN stays NaN.  When the scale grows, the rows before the first
+ * new one are rounded again to the new scale (exact but for values that become subnormal); the
+ * rows behind the last new one are left as they were.
+ * The rows of one page must stand together in slot, in ascending order, each once (as
+ * hcl_page_plan writes them); a page that stands in two places is written in no defined order.
+ * Slots beyond the cache are skipped: HCL_ERR_DEVICE_FAULT.
+ */
+HCL_API hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const void* v_new,
+                                     int64_t v_stride, const int32_t* slot, int T,
+                                     const hcl_paged_kv_t* kv, int32_t* status, void* stream);
+
+/*
+ * hcl_paged_attn -- attention of a ragged batch over the pages, one softmax per query and head.
+ * Request b's queries are rows cu_q[b] .. cu_q[b + 1] - 1 of q; the i-th stands at position
+ * p = q_start[b] + i.  Row j of request b is visible to it when
+ *     j < kv_len[b],   m * (j + 1) - 1 <= p,   and, with W > 0,   j > p - W
+ * (m = 1: raw tokens, causal, optionally a sliding window; m = 128: compressed entries, causal
+ * at entry granularity; W > 0 needs m == 1).  Query head h reads KV head h / (H / Hkv):
+ *     z_j = scale * q . k_j;  out = sum_j softmax(z)_j v_j;  lse = log sum exp z
+ * with the sink as in hcl_csa_sparse_attn.  No rows and no sink: out = 0, lse = -inf.
+ *   q bf16 [T, H, d], token stride q_stride elements (>= H * d, a multiple of 8); cu_q int32
+ *   [B + 1] ascending; q_start, kv_len int32 [B]; table int32 [B, max_pages]; out bf16
+ *   [T, H, d]; lse fp32 [T, H] or NULL.  Rows of out and lse that belong to no request (behind
+ *   cu_q[B]) are left as they were.  max_q: no request has more queries than this (it only
+ *   chooses the kernels; a request with more gets no output and HCL_ERR_DEVICE_FAULT).
+ *   ws: hcl_paged_attn_workspace_bytes() bytes of scratch, its contents unspecified before and
+ *   after; two calls that may overlap need one each.
+ * Page scales must be positive and finite; those below 2^-126 count as 2^-126.  Pages outside
+ * the cache, and rows beyond max_pages * page, are left out: HCL_ERR_DEVICE_FAULT.  Rows at or
+ * behind kv_len, and pages that no query of the request sees, are not read into the result,
+ * whatever their codes.
+ * Supported: H a multiple of Hkv, H / Hkv <= 128, B <= 8192.  The result is bitwise
+ * reproducible for the same lengths; it may depend on the other requests of the batch, whose
+ * lengths set where a long request is split.
+ */
+HCL_API size_t hcl_paged_attn_workspace_bytes(int T, int H, int Hkv, int d);
+HCL_API hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int H,
+                                    const int32_t* cu_q, const int32_t* q_start, int B,
+                                    const hcl_paged_kv_t* kv, const int32_t* table, int max_pages,
+                                    const int32_t* kv_len, int max_q, int m, int W, float scale,
+                                    const float* sink, void* out, float* lse, void* ws,
+                                    size_t ws_bytes, int32_t* status, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * Failure-detection self-test: launches one block whose bounded wait on an mbarrier that

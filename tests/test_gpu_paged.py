@@ -1,0 +1,591 @@
+"""The paged 8-bit cache on the GPU against plain references in 64 bits: page plan, write,
+attention, refusals of the binding, and a run of them together."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+def status():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------------------------ plan
+
+
+class PlanState:
+    def __init__(self, B, width, n_pages, page, T, rng):
+        self.page, self.T, self.n_pages = page, T, n_pages
+        self.seq = [0] * B
+        self.table = np.full((B, width), -1, np.int32)
+        self.stack = rng.permutation(n_pages).tolist()
+        self.d_seq, self.d_table = i32(self.seq), i32(self.table)
+        self.d_free, self.d_n = i32(self.stack), i32([n_pages])
+        self.d_cu = i32(np.zeros(B + 1))
+        self.d_pos, self.d_slot = i32(np.zeros(T)), i32(np.zeros(T))
+
+    def step(self, hcl, keep, new, alias=False):
+        want = ref.plan(keep, new, self.seq, self.table, self.stack + [-1] * (self.n_pages - len(self.stack)),
+                        len(self.stack), self.page, self.T)
+        st = status()
+        hcl.hcl_page_plan(self.d_seq if alias else i32(keep), i32(new), self.d_seq, self.d_table, self.d_free,
+                          self.d_n, self.page, self.d_cu, self.d_pos, self.d_slot, status=st)
+        self.seq, self.table, self.stack = want["seq"], want["table"], want["stack"]
+        assert self.d_seq.tolist() == want["seq"]
+        assert np.array_equal(self.d_table.cpu().numpy(), want["table"])
+        assert self.d_n.item() == len(want["stack"])
+        assert self.d_free[:len(want["stack"])].tolist() == want["stack"]
+        assert self.d_cu.tolist() == want["cu"]
+        assert self.d_pos.tolist() == want["pos"]
+        assert self.d_slot.tolist() == want["slot"]
+        assert st.item() == want["status"]
+        return want
+
+
+@pytest.mark.parametrize("B,page,width,T", [(1, 16, 8, 40), (3, 64, 5, 130), (33, 16, 40, 6000), (300, 32, 20, 20000),
+                                            (1500, 128, 3, 9000)])
+def test_plan_steps(hcl, B, page, width, T):
+    """Growth, rollback, replaced requests, idle requests; pages come back and go out again."""
+    rng = np.random.default_rng(B)
+    S = PlanState(B, width, B * width + 3, page, T, rng)
+    most = min(width * page, T // B)
+    S.step(hcl, [0] * B, rng.integers(0, most + 1, B).tolist())
+    for _ in range(6):
+        keep = [int(rng.choice([s, s, max(0, s - 2), 0, rng.integers(0, s + 1)])) for s in S.seq]
+        room = [min(width * page - k, T // B) for k in keep]
+        new = [int(rng.choice([0, min(1, r), rng.integers(0, r + 1)])) for r in room]
+        S.step(hcl, keep, new)
+        held = [p for b, s in enumerate(S.seq) for p in S.table[b, :-(-s // page)].tolist()]
+        assert sorted(held + S.stack) == list(range(S.n_pages))  # every page has one owner
+    S.step(hcl, S.seq, [0] * B, alias=True)
+    if most > 1:
+        S.step(hcl, [min(s, width * page - 1) for s in S.seq], [1] * B)
+
+
+def test_plan_same_step_again(hcl):
+    rng = np.random.default_rng(3)
+    S = PlanState(20, 10, 150, 16, 900, rng)
+    S.step(hcl, [0] * 20, rng.integers(0, 45, 20).tolist())
+    keep, new = [s // 2 for s in S.seq], rng.integers(0, 40, 20).tolist()
+    a = S.step(hcl, keep, new)
+    b = S.step(hcl, keep, new)
+    assert np.array_equal(a["table"], b["table"]) and a["stack"] == b["stack"]
+
+
+def test_plan_short_of_pages(hcl):
+    rng = np.random.default_rng(4)
+    S = PlanState(6, 8, 10, 16, 200, rng)
+    w = S.step(hcl, [0] * 6, [16, 48, 17, 64, 10, 0])      # 1 + 3 + 2 fit in 10; 4 fit; 1 does not
+    assert w["status"] == 32 and w["seq"] == [16, 48, 17, 64, 0, 0]
+    w = S.step(hcl, S.seq, [0, 0, 1, 0, 5, 3])             # growth inside a page needs none
+    assert w["seq"][2] == 18 and w["seq"][4] == 0 and w["status"] == 32
+    w = S.step(hcl, [0, 48, 18, 64, 0, 0], [0, 0, 0, 0, 5, 0])  # a released page serves another request
+    assert w["seq"][4] == 5 and w["status"] == 0
+
+
+def test_plan_beyond_capacity_and_width(hcl):
+    rng = np.random.default_rng(5)
+    S = PlanState(4, 2, 20, 16, 50, rng)
+    w = S.step(hcl, [0] * 4, [20, 33, 20, 1])   # request 1 is longer than its table row; 2 and 3 end beyond T
+    assert w["status"] == 32 and w["seq"] == [20, 0, 0, 0] and S.d_cu.tolist() == [0, 20, 50, 50, 50]
+    w = S.step(hcl, [25, -1, 0, 0], [-3, 4, 2, 2])
+    assert w["status"] == 16 and w["seq"] == [20, 4, 2, 2]
+
+
+def test_plan_no_requests_no_rows(hcl):
+    empty = torch.zeros(0, dtype=torch.int32, device=DEV)
+    cu, pos, slot = i32([7]), i32([5, 5]), i32([5, 5])
+    hcl.hcl_page_plan(empty, empty, empty, torch.zeros(0, 3, dtype=torch.int32, device=DEV), i32([1, 2]), i32([2]),
+                      16, cu, pos, slot)
+    assert cu.tolist() == [0] and pos.tolist() == [-1, -1] and slot.tolist() == [-1, -1]
+
+
+def test_plan_captured_steps(hcl):
+    """One captured decode step, replayed: the state moves on in place."""
+    rng = np.random.default_rng(6)
+    S = PlanState(5, 6, 40, 16, 5, rng)
+    new = i32([1] * 5)
+
+    def call():
+        hcl.hcl_page_plan(S.d_seq, new, S.d_seq, S.d_table, S.d_free, S.d_n, 16, S.d_cu, S.d_pos, S.d_slot)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for n in range(35):
+        g.replay()
+    assert S.d_seq.tolist() == [35] * 5 and S.d_pos.tolist() == [34] * 5
+    held = S.d_table[:, :3].flatten().tolist() + S.d_free[:S.d_n.item()].tolist()
+    assert sorted(held) == list(range(40))
+
+
+# ------------------------------------------------------------------------------------ write
+
+
+def codes_of(n_pages, Hkv, page, d, gen, scale=100.0):
+    x = torch.randn(n_pages, Hkv, page, d, generator=gen) * scale
+    return x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def check_write(hcl, x, slot, codes, scale, xv=None, cv=None, sv=None):
+    """Runs the write on copies and compares codes and scales exactly."""
+    c, s = codes.cuda(), scale.cuda()
+    c2, s2 = (None, None) if cv is None else (cv.cuda(), sv.cuda())
+    st = status()
+    store = hcl.PagedKV(c, s, c2, s2)
+    hcl.hcl_paged_write(x, xv, i32(slot), store, status=st)
+    assert st.item() == 0
+    for xx, c0, s0, c1, s1 in ((x, codes, scale, c, s), (xv, cv, sv, c2, s2)):
+        if xx is None:
+            continue
+        val, want = ref.write(ref.f64(xx), slot, c0.numpy(), s0.numpy())
+        np.testing.assert_array_equal(ref.f64(s1), want)
+        np.testing.assert_array_equal(ref.decode_e4m3(c1.cpu().numpy()), val)
+    return store
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hkv,both", [(1, False), (2, True), (5, True)])
+def test_write(hcl, d, page, Hkv, both):
+    """Prompts from a page's middle and start, single rows, padding; scales that grow and do not."""
+    gen = torch.Generator().manual_seed(page + d)
+    n_pages = 14
+    perm = torch.randperm(n_pages, generator=gen).tolist()
+    slot = []
+    for first, n in ((page // 2 + 1, 2 * page + 3), (0, page), (page - 1, 1), (3, 2), (0, 1)):
+        own = [perm.pop() for _ in range(-(-(first + n) // page))]
+        slot += [own[p // page] * page + p % page for p in range(first, first + n)]
+        slot += [-1]
+    T = len(slot)
+
+    def rows():
+        big = torch.exp2(torch.randn(T, Hkv, 1, generator=gen) * 3)
+        return (torch.randn(T, Hkv, d, generator=gen) * big).to(torch.bfloat16).cuda()
+
+    def scales():
+        return torch.exp2(torch.randint(-9, 0, (n_pages, Hkv), generator=gen).float())
+
+    args = (codes_of(n_pages, Hkv, page, d, gen), scales())
+    more = (rows(), codes_of(n_pages, Hkv, page, d, gen), scales()) if both else ()
+    check_write(hcl, rows(), slot, *args, *more)
+
+
+def test_write_special_values(hcl):
+    """Infinities saturate and do not set the scale, NaN stays NaN, zeros and subnormals; a scale
+    that is no power of two is kept until it grows."""
+    page, d = 16, 64
+    gen = torch.Generator().manual_seed(1)
+    x = torch.randn(8, 1, d, generator=gen)
+    x[0, 0, :4] = torch.tensor([math.inf, -math.inf, math.nan, 448.0])
+    x[1] = 0.0
+    x[2] = 1e-40                  # bf16 subnormals
+    x[3, 0, 0] = 3.3e38           # near the largest bf16
+    x[4, 0, 0] = 1.75             # 448 * 2^-8 exactly
+    x[5, 0, 0] = 1.7578125        # the next bf16 above
+    x[4, 0, 1:] *= 0.01
+    x[5, 0, 1:] *= 0.01
+    x = x.to(torch.bfloat16).cuda()
+    codes = codes_of(10, 1, page, d, gen)
+    scale = torch.full((10, 1), 0.3)
+    slot = [0, 16, 32, 48, 64, 80, 96 + 5, 112 + 15]
+    store = check_write(hcl, x, slot, codes, scale)
+    got = store.k_scale.flatten().tolist()
+    assert got[1] == 2.0 ** -126 and got[4] == 2.0 ** -8 and got[5] == 2.0 ** -7
+    assert got[6] == torch.tensor(0.3).item()
+
+
+def test_write_rows_behind_stay(hcl):
+    gen = torch.Generator().manual_seed(2)
+    codes = codes_of(2, 2, 32, 128, gen)
+    codes[:, :, 20:] = 0x7F
+    x = (torch.randn(3, 2, 128, generator=gen) * 1000).to(torch.bfloat16).cuda()
+    store = check_write(hcl, x, [32 + 17, 32 + 18, 32 + 19], codes, torch.ones(2, 2))
+    assert bool((store.k[:, :, 20:] == 0x7F).all()) and torch.equal(store.k[0].cpu(), codes[0])
+
+
+def test_write_slice_of_wider_rows_and_stream(hcl):
+    gen = torch.Generator().manual_seed(7)
+    wide = torch.randn(40, 6 * 64, generator=gen).to(torch.bfloat16).cuda()
+    k, v = wide[:, 128:256].view(40, 2, 64), wide[:, 256:].view(40, 2, 64)
+    codes, scale = codes_of(4, 2, 16, 64, gen), torch.ones(4, 2)
+    slot = list(range(5, 45))
+    side = torch.cuda.Stream()
+    c, c2 = codes.cuda(), codes.cuda()
+    s, s2 = scale.cuda(), scale.cuda()
+    store = hcl.PagedKV(c, s, c2, s2)
+    sl = i32(slot)
+    side.wait_stream(torch.cuda.current_stream())
+    hcl.hcl_paged_write(k, v, sl, store, stream=side)
+    side.synchronize()
+    for xx, c1, s1 in ((k, c, s), (v, c2, s2)):
+        val, want = ref.write(ref.f64(xx), slot, codes.numpy(), scale.numpy())
+        np.testing.assert_array_equal(ref.decode_e4m3(c1.cpu().numpy()), val)
+        np.testing.assert_array_equal(ref.f64(s1), want)
+
+
+def test_write_slot_beyond_cache(hcl):
+    gen = torch.Generator().manual_seed(8)
+    codes = codes_of(2, 1, 16, 64, gen)
+    c, s, st = codes.cuda(), torch.ones(2, 1, device=DEV), status()
+    x = torch.randn(3, 1, 64, generator=gen).to(torch.bfloat16).cuda()
+    hcl.hcl_paged_write(x, None, i32([32, 2 ** 31 - 1, 16]), hcl.PagedKV(c, s), status=st)
+    assert st.item() == 16
+    assert torch.equal(c[0].cpu(), codes[0]) and not torch.equal(c[1, :, :1].cpu(), codes[1, :, :1])
+
+
+def test_write_far_into_a_large_cache(hcl):
+    """Code offsets beyond 32 bits."""
+    n_pages = (1 << 32) // (128 * 128) + 8
+    c = torch.zeros(n_pages, 1, 128, 128, dtype=torch.uint8, device=DEV)
+    s = torch.ones(n_pages, 1, device=DEV)
+    x = torch.randn(130, 1, 128, device=DEV).to(torch.bfloat16)
+    last = n_pages - 2
+    slot = [last * 128 + 127] + [(last + 1) * 128 + i for i in range(128)] + [0]
+    hcl.hcl_paged_write(x, None, i32(slot), hcl.PagedKV(c, s))
+    for row, sl in ((0, slot[0]), (64, slot[64]), (129, 0)):
+        val = ref.decode_e4m3(c[sl // 128, 0, sl % 128].cpu().numpy()) * s[sl // 128, 0].item()
+        np.testing.assert_allclose(val, ref.f64(x[row, 0]), rtol=2.0 ** -4, atol=s[sl // 128, 0].item() * 2.0 ** -10)
+    assert int((c[1:last] != 0).sum()) == 0
+
+
+# ------------------------------------------------------------------------------------ attention
+
+
+def make_cache(lens, page, Hkv, d, shared, gen, spare=3, nan_tail=True):
+    per = [max(0, -(-n // page)) for n in lens]
+    n_pages = sum(per) + spare
+    order = torch.randperm(n_pages, generator=gen).tolist()
+    table = np.full((len(lens), max(per + [1]) + 1), -1, np.int32)
+    for b, n in enumerate(per):
+        table[b, :n] = [order.pop() for _ in range(n)]
+
+    def plane():
+        return (codes_of(n_pages, Hkv, page, d, gen),
+                torch.exp2(torch.randint(-9, -4, (n_pages, Hkv), generator=gen).float()))
+
+    k, ks = plane()
+    v, vs = (None, None) if shared else plane()
+    if nan_tail:  # rows behind a request's last, and pages of no request, hold NaN codes
+        for b, n in enumerate(lens):
+            if n % page:
+                for c in (k, v):
+                    if c is not None:
+                        c[table[b, n // page], :, n % page:] = 0x7F
+        for pg in order:
+            for c in (k, v):
+                if c is not None:
+                    c[pg] = 0xFF
+    return table, k, ks, v, vs
+
+
+def tolerance(want, mass, zabs):
+    """bf16 output: half a step, 2^-8 |out|.  Probabilities in 11 bits: 2^-11 of each term, so
+    2^-11 mass, twice that for the smallest; scores: products of codes and bf16 are exact, their
+    fp32 sum over d <= 128 terms is off by at most 128 * 2^-24 of zabs, as is the exponent's
+    argument, and moves each probability by twice that."""
+    return 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2.0 ** -15 * zabs[..., None]) * mass + 1e-30
+
+
+def check_attn(hcl, case, seed=0, poison=None, **kw):
+    """case: lens, news, start (None: the last queries), Hkv, G, d, page, shared, m, W, sink."""
+    gen = torch.Generator().manual_seed(seed)
+    lens, news, Hkv, G, d, page = (case[k] for k in ("lens", "news", "Hkv", "G", "d", "page"))
+    m, W = case.get("m", 1), case.get("W", 0)
+    start = case.get("start") or [l * m - n for l, n in zip(lens, news)]
+    H = Hkv * G
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(int)
+    T = int(cu[-1]) + case.get("pad", 0)
+    table, k, ks, v, vs = make_cache(lens, page, Hkv, d, case.get("shared", False), gen)
+    q = (torch.randn(T, H, d, generator=gen) * case.get("qs", 1.5)).to(torch.bfloat16)
+    sink = torch.randn(H, generator=gen) if case.get("sink") else None
+    if poison:
+        poison(table, k, ks, v, vs, q)
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    store = hcl.PagedKV(dev(k), dev(ks), dev(v), dev(vs))
+    out = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((T, H), 7.0, device=DEV)
+    st = status()
+    scale = case.get("scale", 1 / math.sqrt(d))
+    args = (i32(cu), i32(start), store, i32(table), i32(lens))
+    hcl.hcl_paged_attn(q.cuda(), *args, out, lse=lse, m=m, W=W, scale=scale, sink=dev(sink), status=st,
+                       max_q=case.get("max_q", max(news + [0])), **kw)
+    torch.cuda.synchronize()
+    assert st.item() == case.get("status", 0)
+    want, wl, mass, zabs = ref.attn(ref.f64(q), cu, start, lens, np.maximum(table, 0), k.numpy(), ks.numpy(),
+                                    None if v is None else v.numpy(), None if vs is None else vs.numpy(), page, m, W,
+                                    scale, sink)
+    got, gl = ref.f64(out), ref.f64(lse)
+    n = int(cu[-1])
+    assert np.all(got[n:] == 7.0) and np.all(gl[n:] == 7.0)
+    return got[:n], gl[:n], want[:n], wl[:n], mass[:n], zabs[:n]
+
+
+def assert_attn(got, gl, want, wl, mass, zabs):
+    assert np.array_equal(np.isneginf(wl), np.isneginf(gl)) and not np.isnan(gl).any()
+    fin = np.isfinite(wl)
+    assert np.all(np.abs(gl - wl)[fin] <= (2.0 ** -16 * zabs + 2.0 ** -19 * (1 + np.abs(wl)))[fin])
+    assert np.all(got[~fin] == 0.0)
+    bad = np.abs(got - want) > tolerance(want, mass, zabs)
+    assert not bad.any(), (np.argwhere(bad)[:5], np.abs(got - want).max())
+
+
+CASES = {
+    "one_token": dict(lens=[1], news=[1], Hkv=1, G=1, d=128, page=16),
+    "decode_gqa": dict(lens=[1, 63, 64, 65, 127, 200, 500], news=[1] * 7, Hkv=2, G=8, d=128, page=64),
+    "decode_g5_d64": dict(lens=[3, 130, 257], news=[1] * 3, Hkv=3, G=5, d=64, page=16),
+    "decode_mha": dict(lens=[40, 333], news=[1, 1], Hkv=4, G=1, d=64, page=32),
+    "decode_shared16": dict(lens=[100, 513, 1], news=[1] * 3, Hkv=1, G=16, d=128, page=128, shared=True, sink=True),
+    "decode_g24": dict(lens=[300, 77], news=[1] * 2, Hkv=2, G=24, d=128, page=64),
+    "decode_mqa128": dict(lens=[300, 1, 129], news=[1] * 3, Hkv=1, G=128, d=128, page=64, shared=True, sink=True),
+    "decode_mqa64_d64": dict(lens=[700, 15], news=[1] * 2, Hkv=1, G=64, d=64, page=16),
+    "draft": dict(lens=[5, 64, 300], news=[4, 3, 4], Hkv=2, G=4, d=64, page=16),
+    "draft_mqa": dict(lens=[50, 260], news=[3, 2], Hkv=1, G=64, d=128, page=32, shared=True),
+    "empty_requests": dict(lens=[0, 50, 0, 20, 0], news=[1, 0, 0, 2, 1], start=[-1, 50, 0, 18, 0], Hkv=2, G=2, d=128,
+                           page=16, pad=3),
+    "prompt": dict(lens=[150, 31, 128], news=[150, 31, 128], Hkv=2, G=4, d=128, page=64),
+    "prompt_d64": dict(lens=[150, 300], news=[150, 97], Hkv=1, G=7, d=64, page=32, sink=True),
+    "chunk_shared": dict(lens=[700], news=[100], Hkv=1, G=16, d=128, page=64, shared=True),
+    "mixed": dict(lens=[400, 90, 256, 10], news=[1, 90, 40, 1], Hkv=2, G=8, d=128, page=16, pad=5),
+    "mixed_d64": dict(lens=[400, 90, 256, 10], news=[1, 90, 40, 1], Hkv=2, G=4, d=64, page=128, pad=1),
+    "window_decode": dict(lens=[300, 5, 128, 129], news=[1] * 4, Hkv=1, G=8, d=128, page=16, W=128),
+    "window_one": dict(lens=[40, 100], news=[7, 100], Hkv=1, G=4, d=128, page=16, W=1),
+    "window_prompt": dict(lens=[700, 257], news=[300, 257], Hkv=1, G=16, d=128, page=32, W=128, shared=True, sink=True),
+    "entries_m128": dict(lens=[5, 40], news=[300, 1], start=[100, 40 * 128 - 1], Hkv=1, G=16, d=128, page=16, m=128,
+                         shared=True),
+    "entries_m4": dict(lens=[64, 20], news=[70, 81], start=[186, 0], Hkv=2, G=3, d=64, page=16, m=4, sink=True),
+    "rows_see_nothing": dict(lens=[30, 30], news=[40, 3], start=[-35, -2], Hkv=1, G=2, d=64, page=16),
+    "held_but_ahead": dict(lens=[100, 300], news=[5, 200], start=[20, 10], Hkv=2, G=2, d=128, page=16),
+    "behind_the_rows": dict(lens=[20, 200], news=[4, 60], start=[50, 190], Hkv=1, G=8, d=128, page=32, W=64),
+    "window_past_all": dict(lens=[20], news=[4], start=[500], Hkv=1, G=8, d=128, page=32, W=64),
+    "sharp": dict(lens=[260, 100], news=[1, 100], Hkv=1, G=8, d=128, page=64, qs=20.0),
+    "loose_max_q": dict(lens=[260, 100], news=[1, 60], Hkv=1, G=8, d=128, page=64, max_q=1000),
+}
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_attn(hcl, name):
+    assert_attn(*check_attn(hcl, CASES[name], seed=len(name)))
+
+
+@pytest.mark.parametrize("G,new", [(8, 1), (128, 1), (8, 60)])
+def test_attn_page_scales_far_apart(hcl, G, new):
+    """Value scales that span 2^40: each page's weight is kept to its own precision."""
+    def poison(table, k, ks, v, vs, q):
+        n = vs.shape[0]
+        vs[:] = torch.exp2(torch.arange(n).float() * (40.0 / n) - 30)[:, None]
+        ks[:] = 0.01
+    assert_attn(*check_attn(hcl, dict(lens=[300], news=[new], Hkv=1, G=G, d=128, page=16), poison=poison))
+
+
+@pytest.mark.parametrize("G,new", [(8, 1), (64, 1), (8, 90)])
+def test_attn_query_range(hcl, G, new):
+    """Query rows from 2^-60 to 2^60 times the ordinary, with matching scales' effect; a zero row."""
+    def poison(table, k, ks, v, vs, q):
+        q[:, 0] *= 2.0 ** -60
+        q[:, 1] = 0
+        q[:, 2] *= 2.0 ** 4
+    assert_attn(*check_attn(hcl, dict(lens=[200], news=[new], Hkv=1, G=G, d=128, page=32), poison=poison))
+    def tiny(table, k, ks, v, vs, q):
+        q *= 2.0 ** 60
+        ks *= 2.0 ** -60
+    assert_attn(*check_attn(hcl, dict(lens=[200], news=[new], Hkv=1, G=G, d=128, page=32), poison=tiny))
+
+
+@pytest.mark.parametrize("G,news,shared", [(8, [1, 1], False), (128, [1, 1], True), (16, [60, 80], True),
+                                           (8, [100, 30], False)])
+def test_attn_nan_row_reaches_only_those_who_see_it(hcl, G, news, shared):
+    """A NaN code in a key or value row: the queries that see the row become NaN, no others."""
+    lens, page = [120, 100], 16
+    at = [lens[0] - max(1, news[0] // 2), None]  # row of request 0
+    case = dict(lens=lens, news=news, Hkv=1, G=G, d=128, page=page, shared=shared)
+
+    def poison(table, k, ks, v, vs, q):
+        (k if v is None else v)[table[0, at[0] // page], 0, at[0] % page, 5] = 0x7F
+
+    got, gl, want, wl, mass, zabs = check_attn(hcl, case, poison=poison)
+    sees = np.zeros(got.shape[0], bool)
+    for i in range(news[0]):
+        sees[i] = lens[0] - news[0] + i >= at[0]
+    assert sees.any()
+    assert np.isnan(got[sees][:, :, 5]).all() and not np.isnan(got[~sees]).any()
+    ok = ~sees
+    assert_attn(got[ok], gl[ok], want[ok], wl[ok], mass[ok], zabs[ok])
+
+
+@pytest.mark.parametrize("G,new", [(8, 1), (128, 1), (8, 200)])
+def test_attn_bad_page_is_left_out(hcl, G, new):
+    """A page id outside the cache: its rows do not count, the status says so."""
+    gen = torch.Generator().manual_seed(5)
+    lens, page, d = [300], 16, 128
+    table, k, ks, v, vs = make_cache(lens, page, 1, d, False, gen)
+    q = torch.randn(new, G, d, generator=gen).to(torch.bfloat16)
+    for bad in (-1, k.shape[0], 2 ** 31 - 1):
+        t2 = table.copy()
+        t2[0, 3] = bad
+        out, lse, st = torch.empty(new, G, d, dtype=torch.bfloat16, device=DEV), torch.empty(new, G, device=DEV), status()
+        hcl.hcl_paged_attn(q.cuda(), i32([0, new]), i32([300 - new]),
+                           hcl.PagedKV(k.cuda(), ks.cuda(), v.cuda(), vs.cuda()), i32(t2), i32(lens), out, lse=lse,
+                           max_q=new, status=st)
+        assert st.item() == 16
+        # the reference over a cache without that page's rows; queries stand behind or inside all others
+        keep = [j for j in range(19) if j != 3]
+        t3 = table[:, keep]
+        w, wl, mass, zabs = ref.attn(ref.f64(q)[-1:], [0, 1], [300 - 16 - 1], [300 - 16], t3, k.numpy(), ks.numpy(),
+                                     v.numpy(), vs.numpy(), page, 1, 0, 1 / math.sqrt(d))
+        assert_attn(ref.f64(out)[-1:], ref.f64(lse)[-1:], w, wl, mass, zabs)
+
+
+def test_attn_length_beyond_table(hcl):
+    """kv_len beyond the table's row: the rows there are, and the status."""
+    case = dict(lens=[100], news=[1], Hkv=1, G=8, d=64, page=16)
+    gen = torch.Generator().manual_seed(5)
+    table, k, ks, v, vs = make_cache([112], 16, 1, 64, True, gen, nan_tail=False)
+    q = torch.randn(1, 8, 64, generator=gen).to(torch.bfloat16)
+    out, st = torch.empty(1, 8, 64, dtype=torch.bfloat16, device=DEV), status()
+    hcl.hcl_paged_attn(q.cuda(), i32([0, 1]), i32([10 ** 6]), hcl.PagedKV(k.cuda(), ks.cuda()), i32(table[:, :7]),
+                       i32([10 ** 9]), out, max_q=1, status=st)
+    assert st.item() == 16
+    w, wl, mass, zabs = ref.attn(ref.f64(q), [0, 1], [10 ** 6], [112], table, k.numpy(), ks.numpy(), None, None, 16, 1,
+                                 0, 1 / 8.0)
+    assert np.all(np.abs(ref.f64(out) - w) <= tolerance(w, mass, zabs))
+    del case
+
+
+def test_attn_more_queries_than_max_q(hcl):
+    gen = torch.Generator().manual_seed(6)
+    table, k, ks, v, vs = make_cache([64, 64], 16, 1, 64, True, gen)
+    q = torch.randn(6, 8, 64, generator=gen).to(torch.bfloat16).cuda()
+    out, st = torch.full((6, 8, 64), 3.0, dtype=torch.bfloat16, device=DEV), status()
+    hcl.hcl_paged_attn(q, i32([0, 5, 6]), i32([59, 63]), hcl.PagedKV(k.cuda(), ks.cuda()), i32(table), i32([64, 64]),
+                       out, max_q=4, status=st)
+    assert st.item() == 16 and bool((out[:5] == 3.0).all()) and not bool((out[5] == 3.0).all())
+
+
+@pytest.mark.parametrize("G,d,lens,news,shared", [(8, 128, [9000, 20000, 100], [1, 1, 1], False),
+                                                  (128, 128, [9000, 5000], [1, 1], True),
+                                                  (4, 64, [20000], [1], False)])
+def test_attn_long_split(hcl, G, d, lens, news, shared):
+    """Requests long enough to be split over many blocks, and the same bits every time."""
+    case = dict(lens=lens, news=news, Hkv=1, G=G, d=d, page=64, shared=shared)
+    a = check_attn(hcl, case)
+    assert_attn(*a)
+    b = check_attn(hcl, case)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("G,news", [(8, [1, 1, 1]), (8, [1, 70, 1]), (64, [1, 1, 1])])
+def test_attn_slice_of_wider_rows_stream_and_graph(hcl, G, news):
+    """q as a slice of a fused projection, a side stream, then a captured call replayed with other
+    lengths, another table and a used workspace."""
+    gen = torch.Generator().manual_seed(9)
+    lens, page, d = [200, 90, 33], 16, 128
+    T = sum(news)
+    cu = np.concatenate([[0], np.cumsum(news)])
+    table, k, ks, v, vs = make_cache(lens, page, 1, d, False, gen)
+    wide = torch.randn(T, (G + 2) * d, generator=gen).to(torch.bfloat16).cuda()
+    q = wide[:, :G * d].view(T, G, d)
+    store = hcl.PagedKV(k.cuda(), ks.cuda(), v.cuda(), vs.cuda())
+    out, lse = torch.empty(T, G, d, dtype=torch.bfloat16, device=DEV), torch.empty(T, G, device=DEV)
+    d_cu, d_start, d_len, d_table = i32(cu), i32([l - n for l, n in zip(lens, news)]), i32(lens), i32(table)
+    ws = torch.full((max(16, hcl.paged_attn_workspace_bytes(T, G, 1, d)),), 0xFF, dtype=torch.uint8, device=DEV)
+
+    def call(stream=None, ws=ws):
+        hcl.hcl_paged_attn(q, d_cu, d_start, store, d_table, d_len, out, lse=lse, max_q=max(news), ws=ws,
+                           stream=stream)
+
+    def check(lens, tab):
+        w, wl, mass, zabs = ref.attn(ref.f64(q), cu, [l - n for l, n in zip(lens, news)], lens, tab, k.numpy(),
+                                     ks.numpy(), v.numpy(), vs.numpy(), page, 1, 0, 1 / math.sqrt(d))
+        assert_attn(ref.f64(out), ref.f64(lse), w, wl, mass, zabs)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(side)
+    side.synchronize()
+    check(lens, table)
+    out.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    call(side, ws=None)
+    side.synchronize()
+    check(lens, table)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for lens2, tab2 in (([120, 80, 20], table), ([90, 72, 33], table[[1, 0, 2]])):
+        d_len.copy_(i32(lens2))
+        d_start.copy_(i32([l - n for l, n in zip(lens2, news)]))
+        d_table.copy_(i32(tab2))
+        out.zero_()
+        ws.fill_(0xA5)
+        g.replay()
+        torch.cuda.synchronize()
+        check(lens2, tab2)
+
+
+def test_attn_far_into_a_large_cache(hcl):
+    """Pages whose codes lie beyond 2^32 bytes, for the row kernel and the tile kernel."""
+    n_pages = (1 << 32) // (128 * 128) + 40
+    c = torch.full((n_pages, 1, 128, 128), 0x7F, dtype=torch.uint8, device=DEV)
+    s = torch.full((n_pages, 1), 2.0 ** -6, device=DEV)
+    gen = torch.Generator().manual_seed(3)
+    tail = codes_of(30, 1, 128, 128, gen)
+    c[-30:] = tail.cuda()
+    ids = np.arange(20, 0, -1, dtype=np.int32)[None]       # within the tail
+    for G in (8, 128):
+        q = torch.randn(1, G, 128, generator=gen).to(torch.bfloat16)
+        out, lse = torch.empty(1, G, 128, dtype=torch.bfloat16, device=DEV), torch.empty(1, G, device=DEV)
+        hcl.hcl_paged_attn(q.cuda(), i32([0, 1]), i32([2499]), hcl.PagedKV(c, s), i32(ids + n_pages - 30), i32([2500]),
+                           out, lse=lse, max_q=1)
+        w, wl, mass, zabs = ref.attn(ref.f64(q), [0, 1], [2499], [2500], ids, tail.numpy(),
+                                     np.full((30, 1), 2.0 ** -6), None, None, 128, 1, 0, 1 / math.sqrt(128))
+        assert_attn(ref.f64(out), ref.f64(lse), w, wl, mass, zabs)
+
+
+# ------------------------------------------------------------------------------------ binding
+
+
+def test_binding_refusals(hcl):
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device=DEV)
+    s = torch.ones(4, 2, device=DEV)
+    with pytest.raises(ValueError):
+        hcl.PagedKV(k, s, k)                       # v without its scale
+    with pytest.raises(ValueError):
+        hcl.PagedKV(k, s[:, :1])
+    with pytest.raises(ValueError):
+        hcl.PagedKV(k.float(), s)
+    with pytest.raises(ValueError):
+        hcl.PagedKV(k.cpu(), s.cpu())
+    store = hcl.PagedKV(k, s)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    ok = dict(q=q, cu_q=i32([0, 3]), q_start=i32([0]), store=store, table=i32([[0, 1]]), kv_len=i32([3]), out=out)
+    hcl.hcl_paged_attn(**ok)
+    for bad in (dict(q=q.float()), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), dict(cu_q=i32([0, 1, 3])),
+                dict(cu_q=ok["cu_q"].long()), dict(kv_len=i32([3]).cpu()), dict(out=out.float()),
+                dict(out=out[:2]), dict(lse=torch.empty(3, 4, dtype=torch.float64, device=DEV)),
+                dict(sink=torch.zeros(3, device=DEV)), dict(W=4, m=2), dict(scale=-1.0), dict(scale=math.nan),
+                dict(q=q[:, :3], out=out[:, :3].contiguous())):
+        with pytest.raises((ValueError, RuntimeError)):
+            hcl.hcl_paged_attn(**{**ok, **bad})
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    hcl.hcl_paged_write(x, None, i32([0, 1, 2]), store)
+    for args in ((x, x, i32([0, 1, 2]), store), (x[:2], None, i32([0, 1, 2]), store),
+                 (x.float(), None, i32([0, 1, 2]), store), (x[:, :1], None, i32([0, 1, 2]), store),
+                 (x, None, torch.tensor([0, 1, 2], device=DEV), store)):
+        with pytest.raises((ValueError, RuntimeError)):
+            hcl.hcl_paged_write(*args)
+    # nothing to do
+    hcl.hcl_paged_write(x[:0], None, i32([]), store)
+    hcl.hcl_paged_attn(q[:0], i32([0, 0]), i32([0]), store, i32([[0, 1]]), i32([3]), out[:0])
