@@ -656,8 +656,8 @@ hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int H, const
   HCL_REQUIRE((long long)T * H < (1ll << 31), "T * H must be below 2^31");
   if (T == 0 || B == 0) return HCL_OK;
   HCL_REQUIRE(q && cu_q && q_start && table && kv_len && out, "NULL pointer");
-  HCL_REQUIRE(max_pages >= 1 && (long long)max_pages * kv->page < (1ll << 31),
-              "max_pages must be positive, max_pages * page below 2^31");
+  HCL_REQUIRE(max_pages >= 1 && (long long)max_pages * kv->page <= (1ll << 30),
+              "max_pages must be positive, max_pages * page at most 2^30");
   HCL_REQUIRE(q_stride >= (int64_t)H * kv->d && q_stride % 8 == 0,
               "q_stride must be >= H * d and a multiple of 8");
   HCL_REQUIRE(aligned16(q) && aligned16(out), "q and out must be 16-byte aligned");

@@ -1,29 +1,19 @@
 // paged_attn.cu -- attention of a ragged batch over the paged 8-bit cache.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 
-#include "hcl_common.cuh"
-#include "hcl_internal.h"
+#include "paged_common.cuh"
 
 namespace hcl {
 namespace {
 
-constexpr float PA_LOG2E = 1.4426950408889634f;
-constexpr float PA_LN2 = 0.6931471805599453f;
-constexpr int PA_WARPS = 8;
+using namespace paged;
 
-struct PaParams {
-  PagedAttnArgs a;
-  int sh;        // log2(page)
-  int G;         // query heads per KV head
-  float scale2;  // scale * log2(e)
-};
+constexpr int PA_WARPS = 8;
 
 // One block per (query, query head): each warp takes every eighth visible row with an online
 // softmax, lanes over the head's dimensions; the warps' partial results merge in shared memory.
 template <int D>
-__global__ void __launch_bounds__(PA_WARPS * 32) paged_attn_rows_kernel(PaParams p) {
+__global__ void __launch_bounds__(PA_WARPS * 32) paged_attn_rows_kernel(Params p) {
   constexpr int E = D / 32;
   __shared__ float s_m[PA_WARPS], s_l[PA_WARPS], s_o[PA_WARPS][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -41,6 +31,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32) paged_attn_rows_kernel(PaParams
     if (tid == 0) report(p.a.status, HCL_ERR_DEVICE_FAULT);
     return;
   }
+  if ((p.a.cu_q[b + 1] - c0) * p.G <= ROWS_SMALL) return;
   const long long pos = (long long)p.a.q_start[b] + (t - c0);
   const long long room = (long long)p.a.max_pages << p.sh;
   long long len = p.a.kv_len[b];
@@ -96,7 +87,7 @@ __global__ void __launch_bounds__(PA_WARPS * 32) paged_attn_rows_kernel(PaParams
   __syncthreads();
   float mt = -INFINITY, lt = 0.f;
   for (int w = 0; w < PA_WARPS; w++) mt = fmaxf(mt, s_m[w]);
-  const float sink2 = p.a.sink ? p.a.sink[h] * PA_LOG2E : -INFINITY;
+  const float sink2 = p.a.sink ? p.a.sink[h] * LOG2E : -INFINITY;
   mt = fmaxf(mt, sink2);
   for (int w = 0; w < PA_WARPS; w++) lt += s_m[w] == -INFINITY ? 0.f : s_l[w] * exp2f(s_m[w] - mt);
   if (sink2 != -INFINITY) lt += exp2f(sink2 - mt);
@@ -107,19 +98,30 @@ __global__ void __launch_bounds__(PA_WARPS * 32) paged_attn_rows_kernel(PaParams
     static_cast<__nv_bfloat16*>(p.a.out)[((size_t)t * p.a.H + h) * D + i] = __float2bfloat16(acc * inv);
   }
   if (tid == 0 && p.a.lse)
-    p.a.lse[(size_t)t * p.a.H + h] = lt > 0.f ? (mt + log2f(lt)) * PA_LN2 : -INFINITY;
+    p.a.lse[(size_t)t * p.a.H + h] = lt > 0.f ? (mt + log2f(lt)) * LN2 : -INFINITY;
 }
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(int, int, int, int) { return 0; }
+size_t paged_attn_workspace_bytes(int, int, int, int d) { return rows_workspace(d); }
 
-hcl_status_t launch_paged_attn(const PagedAttnArgs& a, void*, cudaStream_t st) {
-  PaParams p;
+hcl_status_t launch_paged_attn(const PagedAttnArgs& a, void* ws, cudaStream_t st) {
+  Params p;
   p.a = a;
   p.sh = a.kv.page == 16 ? 4 : a.kv.page == 32 ? 5 : a.kv.page == 64 ? 6 : 7;
   p.G = a.H / a.kv.Hkv;
-  p.scale2 = a.scale * PA_LOG2E;
+  p.scale2 = a.scale * LOG2E;
+  p.limit = wait_limit_cycles();
+  p.n_blocks = rows_blocks();
+  p.meta = static_cast<int4*>(ws);
+  p.part = reinterpret_cast<float*>(p.meta + 2 * p.n_blocks);
+  if (p.G <= ROWS_SMALL) {
+    hcl_status_t e = launch_rows(p, st);
+    if (e != HCL_OK) return e;
+    e = launch_rows_merge(p, st);
+    if (e != HCL_OK) return e;
+  }
+  if ((long long)p.a.max_q * p.G <= ROWS_SMALL) return HCL_OK;
   auto kern = a.kv.d == 128 ? paged_attn_rows_kernel<128> : paged_attn_rows_kernel<64>;
   return check_cuda(launch_pdl(kern, dim3((unsigned)((long long)a.T * a.H)), dim3(PA_WARPS * 32), 0, st, 1, p),
                     "paged attention launch");

@@ -1,0 +1,209 @@
+// paged_common.cuh -- what the paged attention kernels share: the requests as the kernels see
+// them, the split of a ragged batch over the blocks, and the numerics of codes and page scales.
+//
+// Split.  The work is a list of units (a tile of KV rows for one item; an item is a request, a KV
+// head and, in the tile kernel, a tile of query rows).  Block c of n takes units c*U/n ..
+// (c+1)*U/n - 1: equal shares whatever the lengths, each block computing its own bounds from the
+// lengths on the device, so that nothing has to be known on the host and a captured launch can
+// be replayed with other lengths.  A block that does not hold a whole item writes a partial
+// result, "head" (the item began in an earlier block) or "tail" (it began here and does not end
+// here); the merge kernel joins them.
+//
+// Numerics.  Codes are exact in fp16 and so is a query row after its exponent is taken out
+// (2^e with the row's largest magnitude in [2^14, 2^15)), so the fp16 products of Q K^T are
+// exact and summed in fp32:  z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
+// A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + 7) with
+// lv = log2(v_scale) and M >= max(z2 + lv) - 8 a running reference, rounded to fp16 (11 bits,
+// 39 binades below the largest), and O = sum P * code in fp32 needs no further scale.  The
+// softmax sum has its own reference m = max z2 (l = sum 2^(z2 - m)), formed from the unrounded P
+// of each group of 16 rows (never more than one page) times 2^(M - 7 - lv - m).  lv is not taken
+// below the largest lv met so far minus 60 (a page of zeros has the scale 2^-126), which keeps
+// every factor in range; its values then count as less than 2^-60 of the largest page's.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "hcl_common.cuh"
+#include "hcl_internal.h"
+
+namespace hcl {
+namespace paged {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float P_OFF = 7.f;       // P's largest magnitude is 2^P_OFF .. 2^(P_OFF + P_LAZY) <= 2^15
+constexpr float P_LAZY = 8.f;      // M may lag its maximum by this much
+constexpr float LV_SPAN = 60.f;
+constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126
+constexpr int ROWS_SMALL = 16;     // query rows (queries x heads of a KV head) of the row kernel
+
+struct Params {
+  PagedAttnArgs a;
+  int sh;            // log2(page)
+  int G;             // query heads per KV head
+  float scale2;      // scale * log2(e)
+  int n_blocks;      // blocks that share the units
+  float* part;       // partial results
+  int4* meta;        // two per block: its first unit, and the first unit of the item it falls into
+  long long limit;
+};
+
+// One request, bounds applied.
+struct Req {
+  int nq, c0;        // queries (0: nothing to do), row of the first
+  int len;           // rows held
+  int qs;            // position of the first query
+};
+
+// Row range [lo, hi) that query i of a request sees.
+__device__ __forceinline__ int vis_hi(const Params& p, const Req& r, int i) {
+  const long long pos = (long long)r.qs + i;
+  if (pos < 0) return 0;
+  const long long h = p.a.m == 1 ? pos + 1 : (pos + 1) / p.a.m;
+  return (int)min((long long)r.len, h);
+}
+__device__ __forceinline__ int vis_lo(const Params& p, const Req& r, int i) {
+  if (p.a.W == 0) return 0;
+  const long long lo = (long long)r.qs + i - p.a.W + 1;
+  return (int)max(0ll, min(lo, (long long)r.len));
+}
+
+__device__ __forceinline__ Req load_req(const Params& p, int b, bool say) {
+  Req r;
+  int c0 = __ldg(p.a.cu_q + b), c1 = __ldg(p.a.cu_q + b + 1), len = __ldg(p.a.kv_len + b);
+  r.qs = __ldg(p.a.q_start + b);
+  const long long room = (long long)p.a.max_pages << p.sh;
+  int fault = 0;
+  if (c0 < 0 || c1 < c0 || c1 > p.a.T || c1 - c0 > p.a.max_q) {
+    fault = 1;
+    c1 = c0;
+  }
+  if (len > room) {
+    fault = 1;
+    len = (int)room;
+  }
+  r.c0 = c0;
+  r.nq = c1 - c0;
+  r.len = max(len, 0);
+  if (say && fault) report(p.a.status, HCL_ERR_DEVICE_FAULT);
+  return r;
+}
+
+// This block's share of the units.  units(b): those of request b.  Every thread of the block
+// calls it (NT threads, a multiple of 32); s: scratch of NT / 32 + 4 words.
+struct Share {
+  long long u0, u1;  // units [u0, u1)
+  int b;             // the request of u0
+  long long rem;     // u0's place among that request's units
+};
+template <int NT, typename F>
+__device__ __forceinline__ Share find_share(int B, int block, int n_blocks, long long* s, F units) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (B + NT - 1) / NT, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; b++) mine += units(b);
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(~0u, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) s[warp] = inc;
+  __syncthreads();
+  long long off = 0, tot = 0;
+  for (int w = 0; w < NT / 32; w++) {
+    if (w < warp) off += s[w];
+    tot += s[w];
+  }
+  Share r;
+  r.u0 = tot * block / n_blocks;
+  r.u1 = tot * (block + 1) / n_blocks;
+  long long at = off + inc - mine;
+  if (r.u0 < tot && at <= r.u0 && r.u0 < at + mine) {
+    for (int b = b0; b < b1; b++) {
+      const long long u = units(b);
+      if (r.u0 < at + u) {
+        s[NT / 32] = b;
+        s[NT / 32 + 1] = r.u0 - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  r.b = (int)s[NT / 32];
+  r.rem = s[NT / 32 + 1];
+  return r;
+}
+
+// log2 of a page scale (exact for powers of two), the scale not below 2^-126.
+__device__ __forceinline__ float log2_scale(float s) {
+  s = fmaxf(s, SCALE_MIN);
+  const uint32_t u = __float_as_uint(s);
+  return (u & 0x7FFFFFu) == 0 ? float(int(u >> 23) - 127) : log2f(s);
+}
+
+// The power of two that brings a row's largest magnitude into [2^14, 2^15): returns the factor
+// 2^-e and sets back = 2^e.  Zero and non-finite rows keep their values.
+__device__ __forceinline__ float row_factor(float amax, float* back) {
+  const int ex = int(__float_as_uint(amax) >> 23);  // biased exponent
+  if (!(amax > 0.f) || ex == 255) {
+    *back = 1.f;
+    return 1.f;
+  }
+  const int e = min(max(ex - 127 - 14, -126), 113);  // 2^e
+  *back = __uint_as_float(uint32_t(e + 127) << 23);
+  return __uint_as_float(uint32_t(127 - e) << 23);
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two E4M3 codes -> fp16 (exact); NaN codes become NaN.
+__device__ __forceinline__ uint32_t half2_of_codes(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+// 0xFF in every byte of x that is a NaN code (0x7F with either sign).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
+  return __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// The final row from O (value units), l and m (log2 units): factor for O and the log-sum-exp.
+// M: O's reference; the sink's logit in log2 units, or -inf.
+__device__ __forceinline__ float finish_row(float m, float M, float l, float sink2, float* lse) {
+  if (!(l > 0.f) && !(l != l)) {  // no row
+    *lse = sink2 == -INFINITY ? -INFINITY : sink2 * LN2;
+    return 0.f;
+  }
+  const float mm = fmaxf(m, sink2);
+  const float lt = l * exp2f(m - mm) + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - mm));
+  *lse = (mm + log2f(lt)) * LN2;
+  return exp2f(M - P_OFF - mm) / lt;
+}
+
+hcl_status_t launch_rows(const Params& p, cudaStream_t st);   // requests of up to ROWS_SMALL rows
+hcl_status_t launch_rows_merge(const Params& p, cudaStream_t st);
+int rows_blocks();
+size_t rows_workspace(int d);
+// Tensor map of a code plane as rows of d bytes, boxes of `rows` rows.
+hcl_status_t code_map(CUtensorMap* m, const void* codes, const hcl_paged_kv_t& kv, int rows, bool swizzle);
+
+}  // namespace paged
+}  // namespace hcl

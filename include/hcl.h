@@ -418,7 +418,7 @@ HCL_API hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const 
  * the cache, and rows beyond max_pages * page, are left out: HCL_ERR_DEVICE_FAULT.  Rows at or
  * behind kv_len, and pages that no query of the request sees, are not read into the result,
  * whatever their codes.
- * Supported: H a multiple of Hkv, H / Hkv <= 128, B <= 8192.  The result is bitwise
+ * Supported: H a multiple of Hkv, H / Hkv <= 128, B <= 8192, max_pages * page <= 2^30.  The result is bitwise
  * reproducible for the same lengths; it may depend on the other requests of the batch, whose
  * lengths set where a long request is split.
  */
