@@ -36,6 +36,9 @@ constexpr float P_LAZY = 8.f;      // M may lag its maximum by this much
 constexpr float LV_SPAN = 60.f;
 constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126
 constexpr int ROWS_SMALL = 16;     // query rows (queries x heads of a KV head) of the row kernel
+constexpr int ROWS_ITEM = 256;     // query rows of an item of the tile kernel
+// A partial result: (m, M, l, -) of each row, then O of each row.
+__host__ __device__ constexpr size_t part_floats(int rows, int d) { return rows * 4 + rows * (size_t)d; }
 
 struct Params {
   PagedAttnArgs a;
@@ -44,7 +47,8 @@ struct Params {
   float scale2;      // scale * log2(e)
   int n_blocks;      // blocks that share the units
   float* part;       // partial results
-  int4* meta;        // two per block: its first unit, and the first unit of the item it falls into
+  int4* meta;        // two per block: its first unit, the first unit of the item it falls into (64 bits
+                     // each), then request, KV head, whether a split item ends here, its first query row
   long long limit;
 };
 
@@ -198,10 +202,15 @@ __device__ __forceinline__ float finish_row(float m, float M, float l, float sin
   return exp2f(M - P_OFF - mm) / lt;
 }
 
-hcl_status_t launch_rows(const Params& p, cudaStream_t st);   // requests of up to ROWS_SMALL rows
-hcl_status_t launch_rows_merge(const Params& p, cudaStream_t st);
+// Kernels for requests of up to ROWS_SMALL query rows, and of more; how many blocks each runs
+// with, its partial results' bytes, and the merge of the requests that it split.
+hcl_status_t launch_rows(const Params& p, cudaStream_t st);
+hcl_status_t launch_tiles(const Params& p, cudaStream_t st);
 int rows_blocks();
+int tile_blocks();
 size_t rows_workspace(int d);
+size_t tile_workspace(int d);
+hcl_status_t launch_merge(const Params& p, int rows, cudaStream_t st);
 // Tensor map of a code plane as rows of d bytes, boxes of `rows` rows.
 hcl_status_t code_map(CUtensorMap* m, const void* codes, const hcl_paged_kv_t& kv, int rows, bool swizzle);
 

@@ -39,7 +39,6 @@ struct Cfg {
   static constexpr uint32_t MISC = SCRATCH + (NW + 1 + 4) * 8;
   static constexpr uint32_t TOTAL = MISC + 16;
 };
-constexpr size_t PART_FLOATS(int d) { return 16 * 4 + 16 * (size_t)d; }  // (m, M, l, -) rows, O rows
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -152,6 +151,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     reinterpret_cast<int*>(m)[4] = any ? w.b : -1;
     reinterpret_cast<int*>(m)[5] = any ? w.g : 0;
     reinterpret_cast<int*>(m)[6] = any && w.tile > 0 && w.tile + w.count == w.nt;  // a split item ends here
+    reinterpret_cast<int*>(m)[7] = 0;                                              // its first query row
   }
   if (!any) return;
 
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int i = valid ? row / p.G : 0, head = w.g * p.G + (valid ? row % p.G : 0);
         const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
         float f = 1.f, lse = 0.f;
-        float* pp = p.part + (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * PART_FLOATS(D);
+        float* pp = p.part + (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * part_floats(ROWS_SMALL, D);
         if (whole) {
           const float sink2 = p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY;
           f = finish_row(mt[h], Mt[h], lt[h], sink2, &lse);
@@ -485,107 +485,6 @@ __global__ void __launch_bounds__(THREADS, 2)
   } while (walk_next(p, w));
 }
 
-// Joins the partial results of the items that were split: block (c, y) takes the item that ends
-// in block c of the kernel above, rows y, y + gridDim.y, ...; one warp per partial result and
-// row, then a sum over the warps in a fixed order.
-constexpr int MW = 8;
-template <int D>
-__global__ void __launch_bounds__(MW * 32) paged_rows_merge_kernel(const Params p) {
-  __shared__ float s_w[2 * 1024];
-  __shared__ float s_red[MW][3];
-  __shared__ float s_o[MW][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
-  pdl_enter();
-  const long long* mc = reinterpret_cast<const long long*>(p.meta + 2 * c);
-  if (!reinterpret_cast<const int*>(mc)[6]) return;
-  const long long first = mc[1];
-  const int b = reinterpret_cast<const int*>(mc)[4], g = reinterpret_cast<const int*>(mc)[5];
-  // the item began in the last block c0 <= c whose first unit is not behind `first`
-  int lo = 0, hi = c;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (reinterpret_cast<const long long*>(p.meta + 2 * mid)[0] <= first) lo = mid;
-    else hi = mid;
-  }
-  const int c0 = lo, n = c - c0 + 1;
-  auto part = [&](int k) { return p.part + (2 * (size_t)(c0 + k) + (k == 0 ? 1 : 0)) * PART_FLOATS(D); };
-  // blocks with no unit between c0 and c wrote nothing
-  auto used = [&](int k) {
-    if (k == 0 || k == n - 1) return true;
-    return reinterpret_cast<const long long*>(p.meta + 2 * (c0 + k))[0] <
-           reinterpret_cast<const long long*>(p.meta + 2 * (c0 + k + 1))[0];
-  };
-  const Req r = load_req(p, b, false);
-  for (int row = blockIdx.y; row < r.nq * p.G; row += gridDim.y) {
-    float m = -INFINITY, M = -INFINITY;
-    for (int k = tid; k < n; k += MW * 32)
-      if (used(k)) {
-        const float4 h = *reinterpret_cast<const float4*>(part(k) + row * 4);
-        m = fmaxf(m, h.x);
-        M = fmaxf(M, h.y);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-      M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    }
-    if (lane == 0) { s_red[warp][0] = m; s_red[warp][1] = M; }
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < MW; v++) { m = fmaxf(m, s_red[v][0]); M = fmaxf(M, s_red[v][1]); }
-    float l = 0.f;
-    for (int k = tid; k < n; k += MW * 32) {
-      float f = 0.f;
-      if (used(k)) {
-        const float4 h = *reinterpret_cast<const float4*>(part(k) + row * 4);
-        f = h.y == -INFINITY ? 0.f : ex2_ftz(h.y - M);
-        l += h.x == -INFINITY ? h.z : h.z * ex2_ftz(h.x - m);
-      }
-      s_w[k] = f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (lane == 0) s_red[warp][2] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int v = 0; v < MW; v++) l += s_red[v][2];
-    constexpr int E = D / 32;
-    float a[E];
-#pragma unroll
-    for (int e = 0; e < E; e++) a[e] = 0.f;
-#pragma unroll 4
-    for (int k = warp; k < n; k += MW) {
-      const float f = s_w[k];
-      if (f != 0.f) {
-        const float* src = part(k) + 64 + row * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(src + e);
-          a[e] = fmaf(x.x, f, a[e]);
-          a[e + 1] = fmaf(x.y, f, a[e + 1]);
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; e++) s_o[warp][lane * E + e] = a[e];
-    __syncthreads();
-    const int head = g * p.G + row % p.G;
-    const size_t orow = (size_t)(r.c0 + row / p.G) * p.a.H + head;
-    const float sink2 = p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY;
-    float lse;
-    const float f = finish_row(m, M, l, sink2, &lse);
-    for (int e = tid; e < D; e += MW * 32) {
-      float x = 0.f;
-#pragma unroll
-      for (int v = 0; v < MW; v++) x += s_o[v][e];
-      static_cast<__nv_bfloat16*>(p.a.out)[orow * D + e] = __float2bfloat16(f == 0.f ? 0.f : x * f);
-    }
-    if (tid == 0 && p.a.lse) p.a.lse[orow] = lse;
-    __syncthreads();
-  }
-}
-
 template <int D, bool SHARED>
 hcl_status_t launch_t(const Params& p, cudaStream_t st) {
   CUtensorMap tk, tv;
@@ -610,16 +509,11 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
 
 int rows_blocks() { return std::min(1024, 2 * num_sms()); }
 
-size_t rows_workspace(int d) { return 2 * (size_t)rows_blocks() * (PART_FLOATS(d) * 4 + sizeof(int4)); }
+size_t rows_workspace(int d) { return 2 * (size_t)rows_blocks() * (part_floats(ROWS_SMALL, d) * 4 + sizeof(int4)); }
 
 hcl_status_t launch_rows(const Params& p, cudaStream_t st) {
   if (p.a.kv.d == 128) return p.a.kv.v ? launch_t<128, false>(p, st) : launch_t<128, true>(p, st);
   return p.a.kv.v ? launch_t<64, false>(p, st) : launch_t<64, true>(p, st);
-}
-
-hcl_status_t launch_rows_merge(const Params& p, cudaStream_t st) {
-  auto kern = p.a.kv.d == 128 ? paged_rows_merge_kernel<128> : paged_rows_merge_kernel<64>;
-  return check_cuda(launch_pdl(kern, dim3(p.n_blocks, 4), dim3(MW * 32), 0, st, 1, p), "paged attention merge launch");
 }
 
 hcl_status_t code_map(CUtensorMap* m, const void* codes, const hcl_paged_kv_t& kv, int rows, bool swizzle) {

@@ -1,0 +1,693 @@
+// paged_tile.cu -- paged attention for requests with many query rows (queries x heads of one KV
+// head > 16): prompts, chunks, and decode with many heads on one KV head.  tcgen05 tensor cores.
+//
+// One persistent block per SM.  An item is 256 query rows (two tiles of 128, the M of an MMA) of
+// one request and KV head; a round is 128 KV rows.  Roles:
+//   warps 0-3 / 4-7   softmax of tile 0 / 1: one thread per query row; they also load Q and
+//                     write the output
+//   warps 8-11        widening: E4M3 codes from global memory (loaded a round ahead into
+//                     registers) to fp16 tiles in shared memory, 128-byte swizzle.  The same
+//                     layout serves K (K-major B operand of S = Q K^T) and V (MN-major B operand
+//                     of O += P V); rows that are both key and value are widened once.
+//   warp 12           one thread issues every MMA:  PV_0(r), S_0(r+1), PV_1(r), S_1(r+1), so one
+//                     tile's softmax runs under the other tile's MMAs
+// P (fp16) is written over the first half of its S in tensor memory and read there as the A
+// operand.  TMEM: S_0 / P_0, S_1 / P_1, O_0, O_1.
+// An item of at most 128 rows (decode over many heads, a request's last rows) runs in single
+// mode: both softmax groups work on the same rows, group t on the rounds of parity t with its
+// own O, and join at the end, so the pipeline keeps its two streams.
+//
+// Bound by the MMA rate and, equally, the exponentials (256 x 128 a round at 16 a clock take as
+// long as the round's MMAs); decode over many heads by the widening and softmax of each round.
+#include <algorithm>
+
+#include "paged_common.cuh"
+
+namespace hcl {
+namespace paged {
+namespace {
+
+constexpr int TILE = 128;      // KV rows per round, query rows per tile
+constexpr int ITEM = ROWS_ITEM;  // query rows per item
+constexpr int THREADS = 13 * 32;
+constexpr int PRING = 8;       // rounds whose page parameters are kept
+constexpr uint32_t O_COL = 256;
+
+struct RoundPar {              // what the softmax needs of a round's pages (groups of 16 rows)
+  float kc[8], lv[8], wl[8];
+  uint32_t valid[4], poison[4];
+  float lvref;
+  float pad[7];
+};
+
+template <int D, bool SHARED>
+struct Cfg {
+  static constexpr int PIECES = D / 16;               // 16-code pieces of a row
+  static constexpr int RPP = 128 / PIECES;            // rows per pass of the widening threads
+  static constexpr int PASSES = TILE / RPP;
+  static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile, and of a K or V tile
+  static constexpr int NK = SHARED ? 4 : 2;           // K (or shared) tiles in the ring
+  static constexpr int NV = SHARED ? 4 : 2;
+  static constexpr uint32_t K = 2 * QT;
+  static constexpr uint32_t V = SHARED ? K : K + NK * QT;
+  static constexpr uint32_t PAR = K + 4 * QT;
+  static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
+  static constexpr uint32_t BAR = STAT + 128 * 16;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 2 + 2 + 1;
+  static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
+  static constexpr uint32_t MISC = SCRATCH + (13 + 4) * 8;
+  static constexpr uint32_t TOTAL = MISC + 16;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+// D (+)= A B with A (packed fp16 pairs) read from tensor memory.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Barrier `id` over n threads; returns whether any of them passed true.
+__device__ __forceinline__ bool bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(uint32_t(x)), "r"(id), "r"(n) : "memory");
+  return r != 0;
+}
+// bits j with lo <= c0 + j < hi
+__device__ __forceinline__ uint32_t range_mask(int c0, int lo, int hi) {
+  const int a = max(lo - c0, 0), b = min(hi - c0, 32);
+  if (a >= b) return 0u;
+  return (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+// ---- the items -----------------------------------------------------------------------------
+
+__device__ __forceinline__ int tiles_of(const Params& p, const Req& r) {
+  const int rows = r.nq * p.G;
+  return rows <= ROWS_SMALL ? 0 : (rows + ITEM - 1) / ITEM;
+}
+// Rounds of a tile: first KV row (a multiple of TILE) and how many (at least one).
+__device__ __forceinline__ int rounds_of(const Params& p, const Req& r, int tile, int* j0) {
+  const int i0 = tile * ITEM / p.G, i1 = (min(r.nq * p.G, (tile + 1) * ITEM) - 1) / p.G;
+  const int hi = vis_hi(p, r, i1), lo = min(vis_lo(p, r, i0), hi);
+  *j0 = 0;
+  if (hi <= lo) return 1;
+  *j0 = lo / TILE * TILE;
+  return (hi - *j0 + TILE - 1) / TILE;
+}
+
+struct Walk {
+  Req r;
+  int b, g, tile, j0, nt;  // request, KV head, tile; its first KV row and rounds
+  int rd, count;           // this block's rounds of the item: rd .. rd + count - 1 of nt
+  long long left;
+};
+__device__ __forceinline__ void walk_set(const Params& p, Walk& w) {
+  w.count = (int)min((long long)(w.nt - w.rd), w.left);
+  w.left -= w.count;
+}
+__device__ __forceinline__ bool walk_first(const Params& p, const Share& s, Walk& w) {
+  w.left = s.u1 - s.u0;
+  if (w.left <= 0) return false;
+  w.b = s.b;
+  w.r = load_req(p, w.b, false);
+  const int nt = tiles_of(p, w.r);
+  int per = 0, j0;
+  for (int t = 0; t < nt; t++) per += rounds_of(p, w.r, t, &j0);
+  w.g = (int)(s.rem / per);
+  int rem = (int)(s.rem % per);
+  w.tile = 0;
+  while (true) {
+    w.nt = rounds_of(p, w.r, w.tile, &w.j0);
+    if (rem < w.nt) break;
+    rem -= w.nt;
+    w.tile++;
+  }
+  w.rd = rem;
+  walk_set(p, w);
+  return true;
+}
+__device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
+  if (w.left <= 0) return false;
+  if (++w.tile == tiles_of(p, w.r)) {
+    w.tile = 0;
+    if (++w.g == p.a.kv.Hkv) {
+      w.g = 0;
+      do w.r = load_req(p, ++w.b, false);
+      while (tiles_of(p, w.r) == 0);
+    }
+  }
+  w.nt = rounds_of(p, w.r, w.tile, &w.j0);
+  w.rd = 0;
+  walk_set(p, w);
+  return true;
+}
+__device__ __forceinline__ int item_rows(const Params& p, const Walk& w) {
+  return min(ITEM, w.r.nq * p.G - w.tile * ITEM);
+}
+
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) {
+  using C = Cfg<D, SHARED>;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  RoundPar* par = reinterpret_cast<RoundPar*>(sm + C::PAR);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + C::BAR);
+  uint64_t* k_empty = k_full + C::NK;
+  uint64_t* v_full = k_empty + C::NK;
+  uint64_t* v_empty = v_full + C::NV;
+  uint64_t* s_full = v_empty + C::NV;  // [2] S of the step in TMEM
+  uint64_t* p_full = s_full + 2;       // [2] P in TMEM, O rescaled
+  uint64_t* o_done = s_full + 4;       // [2] PV of the step completed
+  uint64_t* q_full = s_full + 6;       // [2] Q tile in shared memory
+  uint64_t* drain = s_full + 8;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + C::MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + C::MISC + 4);
+  if (tid == 0) {
+    for (int i = 0; i < C::NK; i++) { mbar_init(&k_full[i], 128); mbar_init(&k_empty[i], 1); }
+    for (int i = 0; i < C::NV; i++) { mbar_init(&v_full[i], 128); mbar_init(&v_empty[i], 1); }
+    for (int t = 0; t < 2; t++) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&o_done[t], 1);
+      mbar_init(&q_full[t], 128);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_enter();
+  tc_fence_before();
+  const Share share = find_share<THREADS>(p.a.B, blockIdx.x, p.n_blocks, reinterpret_cast<long long*>(sm + C::SCRATCH),
+                                          [&](int b) {
+                                            const Req r = load_req(p, b, blockIdx.x == 0);
+                                            const int nt = tiles_of(p, r);
+                                            long long n = 0;
+                                            int j0;
+                                            for (int t = 0; t < nt; t++) n += rounds_of(p, r, t, &j0);
+                                            return n * p.a.kv.Hkv;
+                                          });
+  tc_fence_after();
+  const uint32_t tbase = *s_tmem;
+  Walk w;
+  const bool any = walk_first(p, share, w);
+  if (tid == 0) {
+    long long* m = reinterpret_cast<long long*>(p.meta + 2 * blockIdx.x);
+    m[0] = share.u0;
+    m[1] = any ? share.u0 - w.rd : share.u0;
+    int* mi = reinterpret_cast<int*>(m);
+    mi[4] = any ? w.b : -1;
+    mi[5] = any ? w.g : 0;
+    mi[6] = any && w.rd > 0 && w.rd + w.count == w.nt;
+    mi[7] = any ? w.tile * ITEM : 0;
+  }
+
+  if (any && warp >= 8 && warp < 12) {
+    // ------------------------------------------------------------------ widening
+    const int wt = tid - 256, pc = wt % C::PIECES, pr = wt / C::PIECES;
+    const uint8_t* kcodes = static_cast<const uint8_t*>(p.a.kv.k);
+    const uint8_t* vcodes = static_cast<const uint8_t*>(p.a.kv.v);
+    const int pmask = p.a.kv.page - 1;
+    bool ok = true, fault = false;
+    uint32_t rg = 0;  // rounds so far
+    do {
+      const int rows = item_rows(p, w), i0 = w.tile * ITEM / p.G, i1 = (w.tile * ITEM + rows - 1) / p.G;
+      const int all_lo = vis_lo(p, w.r, i1), all_hi = vis_hi(p, w.r, i0), any_hi = vis_hi(p, w.r, i1);
+      const int32_t* trow = p.a.table + (size_t)w.b * p.a.max_pages;
+      // page of KV row j: -2 where no row is wanted, -1 for an id outside the cache
+      auto page_at = [&](int j) {
+        int id = j < any_hi ? __ldg(trow + (j >> p.sh)) : -2;
+        if (id != -2 && (id < 0 || id >= p.a.kv.n_pages)) { id = -1; fault = true; }
+        return id;
+      };
+      auto load_ids = [&](int i, int (&id)[C::PASSES]) {
+#pragma unroll
+        for (int q = 0; q < C::PASSES; q++) id[q] = i < w.count ? page_at(w.j0 + (w.rd + i) * TILE + q * C::RPP + pr) : -2;
+      };
+      auto load_codes = [&](const uint8_t* codes, int i, const int (&id)[C::PASSES], uint4 (&x)[C::PASSES]) {
+#pragma unroll
+        for (int q = 0; q < C::PASSES; q++) {
+          const int j = w.j0 + (w.rd + i) * TILE + q * C::RPP + pr;
+          x[q] = make_uint4(0, 0, 0, 0);
+          if (id[q] >= 0 && j < any_hi)
+            x[q] = __ldg(reinterpret_cast<const uint4*>(
+                codes + ((((size_t)id[q] * p.a.kv.Hkv + w.g) << p.sh) + (j & pmask)) * D + pc * 16));
+        }
+      };
+      auto store_tile = [&](uint8_t* tile, const uint4 (&x)[C::PASSES]) {
+#pragma unroll
+        for (int q = 0; q < C::PASSES; q++) {
+          const int row = q * C::RPP + pr;
+          const uint4 lo = make_uint4(half2_of_codes(uint16_t(x[q].x)), half2_of_codes(uint16_t(x[q].x >> 16)),
+                                      half2_of_codes(uint16_t(x[q].y)), half2_of_codes(uint16_t(x[q].y >> 16)));
+          const uint4 hi = make_uint4(half2_of_codes(uint16_t(x[q].z)), half2_of_codes(uint16_t(x[q].z >> 16)),
+                                      half2_of_codes(uint16_t(x[q].w)), half2_of_codes(uint16_t(x[q].w >> 16)));
+          uint8_t* base = tile + (pc >> 2) * 16384 + row * 128;
+          const int c0 = (pc & 3) * 2;
+          uint4* a0 = reinterpret_cast<uint4*>(base + ((c0 ^ (row & 7)) << 4));
+          uint4* a1 = reinterpret_cast<uint4*>(base + (((c0 + 1) ^ (row & 7)) << 4));
+          // the two 64-dimension halves start with different pieces: no bank conflict
+          if (pc & 4) { *a1 = hi; *a0 = lo; }
+          else { *a0 = lo; *a1 = hi; }
+        }
+      };
+      // NaN codes of a round that not all query rows see whole: the value becomes 0 (0 * NaN
+      // would reach rows that do not see it), and the softmax marks the rows that do see it
+      auto clean = [&](uint4 (&x)[C::PASSES], RoundPar* rp) {
+#pragma unroll
+        for (int q = 0; q < C::PASSES; q++) {
+          const uint4 n4 = make_uint4(nan_bytes(x[q].x), nan_bytes(x[q].y), nan_bytes(x[q].z), nan_bytes(x[q].w));
+          if (n4.x | n4.y | n4.z | n4.w) {
+            x[q] = make_uint4(x[q].x & ~n4.x, x[q].y & ~n4.y, x[q].z & ~n4.z, x[q].w & ~n4.w);
+            const int row = q * C::RPP + pr;
+            atomicOr(&rp->poison[row >> 5], 1u << (row & 31));
+          }
+        }
+      };
+      int id[C::PASSES];
+      uint4 kx[C::PASSES], vx[SHARED ? 1 : C::PASSES];
+      load_ids(0, id);
+      load_codes(kcodes, 0, id, kx);
+      if constexpr (!SHARED) load_codes(vcodes, 0, id, vx);
+      // page parameters: lane g8 of the first widening warp has group g8
+      int gid = -2;
+      float gks = 0.f, gvs = 0.f, lvref = -INFINITY;
+      auto load_scales = [&](int i) {
+        const int j = w.j0 + (w.rd + i) * TILE + (lane & 7) * 16;
+        gid = i < w.count ? page_at(j) : -2;
+        if (gid >= 0) {
+          const size_t pg = (size_t)gid * p.a.kv.Hkv + w.g;
+          gks = __ldg(p.a.kv.k_scale + pg);
+          gvs = SHARED ? gks : __ldg(p.a.kv.v_scale + pg);
+        }
+      };
+      if (warp == 8) load_scales(0);
+      for (int i = 0; i < w.count; i++, rg++) {
+        const int kb = rg % C::NK;
+        RoundPar* rp = par + rg % PRING;
+        const int j0 = w.j0 + (w.rd + i) * TILE;
+        const bool edge = j0 < all_lo || j0 + TILE > all_hi;
+        uint64_t* ke = SHARED ? v_empty : k_empty;
+        if (rg >= C::NK) ok = ok && mbar_wait(&ke[kb], ((rg / C::NK) & 1) ^ 1, p.limit, s_abort);
+        if (warp == 8) {
+          const bool good = gid >= 0;
+          float lv = good ? log2_scale(gvs) : -INFINITY, mx = lv;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+          lvref = fmaxf(lvref, mx);
+          const uint32_t gm = __ballot_sync(~0u, good) & 0xFF;
+          if (lane < 8) {
+            lv = fmaxf(lv, lvref - LV_SPAN);
+            rp->kc[lane] = good ? fmaxf(gks, SCALE_MIN) * p.scale2 : 0.f;
+            rp->lv[lane] = good ? lv : 0.f;
+            rp->wl[lane] = good ? ex2_ftz(lvref - lv) : 0.f;
+            if (lane < 4) {
+              rp->valid[lane] = ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
+              rp->poison[lane] = 0u;
+            }
+            if (lane == 0) rp->lvref = lvref == -INFINITY ? 0.f : lvref;
+          }
+        }
+        // the parameters stand before any thread marks a poisoned row
+        if (bar_or(2, 128, !ok)) { ok = false; break; }
+        if (SHARED && edge) clean(kx, rp);
+        store_tile(sm + C::K + kb * C::QT, kx);
+        fence_proxy_async_smem();
+        mbar_arrive(&k_full[kb]);
+        load_ids(i + 1, id);
+        load_codes(kcodes, i + 1, id, kx);
+        if (warp == 8) load_scales(i + 1);
+        if constexpr (!SHARED) {
+          const int vb = rg % C::NV;
+          if (rg >= C::NV) ok = ok && mbar_wait(&v_empty[vb], ((rg / C::NV) & 1) ^ 1, p.limit, s_abort);
+          if (edge) clean(vx, rp);
+          store_tile(sm + C::V + vb * C::QT, vx);
+          fence_proxy_async_smem();
+          mbar_arrive(&v_full[vb]);
+          load_codes(vcodes, i + 1, id, vx);
+        }
+      }
+      ok = !bar_or(2, 128, !ok);  // the four warps go on, or end, together
+    } while (ok && walk_next(p, w));
+    if (!ok) {
+      *s_abort = 1;
+      report(p.a.status, HCL_ERR_TIMEOUT);
+    }
+    if (fault) report(p.a.status, HCL_ERR_DEVICE_FAULT);
+  } else if (any && warp == 12) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t dq = make_sdesc(smem_u32(sm), 16, 1024, SMEM_SWIZZLE_128B);
+      const uint64_t dk = make_sdesc(smem_u32(sm + C::K), 16, 1024, SMEM_SWIZZLE_128B);
+      const uint64_t dv = make_sdesc(smem_u32(sm + C::V), 16384, 1024, SMEM_SWIZZLE_128B);
+      constexpr uint32_t idS = idesc_f16(128, TILE), idPV = idesc_f16(128, D) | (1u << 16);
+      uint32_t rg = 0, step[2] = {0, 0}, items = 0;
+      bool ok = true;
+      do {
+        const int n = w.count;
+        const bool pair = item_rows(p, w) > 128;
+        const int steps[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
+        auto round_of = [&](int t, int k) { return rg + uint32_t(pair ? k : 2 * k + t); };
+        auto issue_s = [&](int t, int k) {
+          const uint32_t R = round_of(t, k), kb = R % C::NK;
+          ok = ok && mbar_wait(&k_full[kb], (R / C::NK) & 1, p.limit, s_abort);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t a0 = dq + uint64_t((pair ? t : 0) * (C::QT >> 4)), b0 = dk + uint64_t(kb * (C::QT >> 4));
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ks++) {
+            const uint32_t off = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
+            umma_bf16(tbase + t * TILE, a0 + off, b0 + off, idS, ks > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[t]);
+          if (!SHARED && (!pair || t == 1)) umma_commit(&k_empty[kb]);
+        };
+        for (int t = 0; t < (pair ? 2 : 1) && ok; t++) ok = mbar_wait(&q_full[t], items & 1, p.limit, s_abort);
+        for (int t = 0; t < 2; t++)
+          if (steps[t] > 0) issue_s(t, 0);
+        for (int k = 0; k < steps[0] && ok; k++) {
+          for (int t = 0; t < 2 && ok; t++) {
+            if (k >= steps[t]) continue;
+            const uint32_t R = round_of(t, k), vb = R % C::NV;
+            ok = mbar_wait(&p_full[t], (step[t] + k) & 1, p.limit, s_abort);
+            if (ok && !SHARED) ok = mbar_wait(&v_full[vb], (R / C::NV) & 1, p.limit, s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t b0 = dv + uint64_t(vb * (C::QT >> 4));
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++)
+              umma_f16_ta(tbase + O_COL + t * 128, tbase + t * TILE + ks * 8, b0 + uint32_t(ks * (2048 >> 4)), idPV,
+                          (k > 0 || ks > 0) ? 1u : 0u);
+            umma_commit(&o_done[t]);
+            if (!pair || t == 1) umma_commit(&v_empty[vb]);
+            if (k + 1 < steps[t]) {
+              // S_t of the next step overwrites P_t: PV_t must have completed
+              ok = mbar_wait(&o_done[t], (step[t] + k) & 1, p.limit, s_abort);
+              issue_s(t, k + 1);
+            }
+          }
+        }
+        rg += n;
+        step[0] += steps[0];
+        step[1] += steps[1];
+        // q_full[1] is used by pairs only; its phase is kept in step by an arrival of the softmax
+        items++;
+      } while (ok && walk_next(p, w));
+      if (!ok) {
+        *s_abort = 1;
+        report(p.a.status, HCL_ERR_TIMEOUT);
+      }
+      // every MMA issued has completed before TMEM may be freed
+      umma_commit(drain);
+      if (!mbar_wait(drain, 0, p.limit, nullptr)) report(p.a.status, HCL_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (any && warp < 8) {
+    // ------------------------------------------------------------------ softmax
+    const int t = warp >> 2, row = tid & 127;
+    const uint32_t lq = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + lq + t * TILE, tO = tbase + lq + O_COL + t * 128;
+    float* s_stat = reinterpret_cast<float*>(sm + C::STAT);
+    uint32_t rg = 0, step = 0;
+    bool ok = true;
+    do {
+      const int n = w.count, rows = item_rows(p, w);
+      const bool pair = rows > 128;
+      const int irow = (pair ? t * 128 : 0) + row;  // row of the item
+      const bool valid = irow < rows;
+      const int qr = w.tile * ITEM + (valid ? irow : 0), qi = qr / p.G, head = w.g * p.G + qr % p.G;
+      const int hi = valid ? vis_hi(p, w.r, qi) : 0, lo = valid ? vis_lo(p, w.r, qi) : 0;
+      // Q row -> fp16 with its exponent taken out (in single mode group 1 only needs the factor)
+      float back;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                                          (int64_t)(w.r.c0 + qi) * p.a.q_stride + head * D);
+        uint4 x[D / 8];
+        float am = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 8; c++) {
+          x[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; k++)
+            am = fmax3(am, fabsf(__uint_as_float(a[k] << 16)), fabsf(__uint_as_float(a[k] & 0xFFFF0000u)));
+        }
+        const float f = row_factor(am, &back);
+        if (pair || t == 0) {
+          uint8_t* qt = sm + t * C::QT;
+#pragma unroll
+          for (int c = 0; c < D / 8; c++) {
+            uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+              a[k] = half2_of(__uint_as_float(a[k] << 16) * f, __uint_as_float(a[k] & 0xFFFF0000u) * f);
+            *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                make_uint4(a[0], a[1], a[2], a[3]);
+          }
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(&q_full[t]);
+      }
+      const int steps = pair ? n : (n + 1 - t) / 2;
+      float m = -INFINITY, M = -INFINITY, l = 0.f;
+      bool sick = false;  // a NaN value in a row that this query sees
+      auto look = [&](uint32_t R, int j0) {
+        const RoundPar* rp = par + R % PRING;
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+          if (rp->poison[v] & range_mask(j0 + 32 * v, lo, hi)) sick = true;
+      };
+      for (int k = 0; k < steps; k++) {
+        const int rr = pair ? k : 2 * k + t;
+        const uint32_t R = rg + rr;
+        const int j0 = w.j0 + (w.rd + rr) * TILE;
+        ok = mbar_wait(&s_full[t], (step + k) & 1, p.limit, s_abort);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        // (S of this step was issued behind PV of the last: that round's poison marks stand)
+        if (k > 0) look(R - (pair ? 1 : 2), j0 - (pair ? 1 : 2) * TILE);
+        const RoundPar* rp = par + R % PRING;
+        uint32_t vb[4];
+#pragma unroll
+        for (int v = 0; v < 4; v++) vb[v] = range_mask(j0 + 32 * v, lo, hi) & rp->valid[v];
+        uint32_t sv[64];
+        float mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
+#pragma unroll
+        for (int hf = 0; hf < 2; hf++) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) tmem_ld16(tS + hf * 64 + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const uint32_t bits = (vb[2 * hf + (q >> 1)] >> (16 * (q & 1))) & 0xFFFFu;
+            float sx = -INFINITY;
+            if (bits == 0xFFFFu) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 2)
+                sx = fmax3(sx, __uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1]));
+            } else if (bits != 0u) {
+#pragma unroll
+              for (int j = 0; j < 16; j++)
+                if ((bits >> j) & 1u) sx = fmaxf(sx, __uint_as_float(sv[16 * q + j]));
+            }
+            const float zx = sx == -INFINITY ? -INFINITY : sx * fmaxf(rp->kc[4 * hf + q] * back, SCALE_MIN);
+            mz = fmaxf(mz, zx);
+            mw = fmaxf(mw, zx + rp->lv[4 * hf + q]);
+          }
+        }
+        const float m2 = fmaxf(m, mz);
+        l *= m2 == m ? 1.f : ex2_ftz(m - m2);
+        m = m2;
+        const float M2 = mw > M + P_LAZY ? mw : M;
+        const float al = M2 == M || M == -INFINITY ? 1.f : ex2_ftz(M - M2);
+        M = M2;
+        // O is stable: S of this step was issued behind the completed PV of the last one
+        if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll
+          for (int q = 0; q < D / 16; q++) {
+            uint32_t r16[16];
+            tmem_ld16(tO + q * 16, r16);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; j++) r16[j] = __float_as_uint(__uint_as_float(r16[j]) * al);
+            tmem_st16(tO + q * 16, r16);
+          }
+        }
+        const float Mu = M == -INFINITY ? 0.f : M, mu = m == -INFINITY ? 0.f : m;
+        // P over S: columns 64c .. 64c + 63 go to columns 32c .. 32c + 31, already read
+        float lr = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) tmem_ld16(tS + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
+          tmem_ld_wait();
+          uint32_t pk[32];
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const uint32_t bits = (vb[2 * c + (q >> 1)] >> (16 * (q & 1))) & 0xFFFFu;
+            const float cc = fmaxf(rp->kc[4 * c + q] * back, SCALE_MIN), add = rp->lv[4 * c + q] - Mu + P_OFF;
+            const unsigned long long c2 = f2_make(cc, cc), a2 = f2_make(add, add);
+            unsigned long long g = 0ull;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const unsigned long long x = f2_fma(
+                  f2_make(__uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1])), c2, a2);
+              float e0 = ex2_ftz(f2_lo(x)), e1 = ex2_ftz(f2_hi(x));
+              if (bits != 0xFFFFu) {
+                e0 = (bits >> j) & 1u ? e0 : 0.f;
+                e1 = (bits >> (j + 1)) & 1u ? e1 : 0.f;
+              }
+              g = f2_add(g, f2_make(e0, e1));
+              pk[8 * q + (j >> 1)] = half2_of(e0, e1);
+            }
+            lr = fmaf(f2_lo(g) + f2_hi(g), rp->wl[4 * c + q], lr);
+          }
+          tmem_st16(tS + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(&pk[0]));
+          tmem_st16(tS + 32 * c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16]));
+        }
+        l = fmaf(lr, ex2_ftz(Mu - P_OFF - rp->lvref - mu), l);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[t]);
+      }
+      if (ok && steps > 0) {
+        ok = mbar_wait(&o_done[t], (step + steps - 1) & 1, p.limit, s_abort);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        if (ok) look(rg + (pair ? n - 1 : 2 * (steps - 1) + t),
+                     w.j0 + (w.rd + (pair ? n - 1 : 2 * (steps - 1) + t)) * TILE);
+      }
+      if (sick) l = NAN;
+      if (!ok) {
+        *s_abort = 1;
+        report(p.a.status, HCL_ERR_TIMEOUT);
+      }
+      // both groups are done with their MMAs (Q's shared memory is free), or the block ends here
+      if (bar_or(3, 256, !ok)) { ok = false; break; }
+      const bool whole = w.count == w.nt;
+      const size_t orow = (size_t)(w.r.c0 + qi) * p.a.H + head;
+      float* pp = p.part + (2 * (size_t)blockIdx.x + (w.rd == 0 ? 1 : 0)) * part_floats(ITEM, D);
+      float mine = 1.f, other = 0.f;  // factors of this group's O and, in single mode, group 1's
+      float* ex = reinterpret_cast<float*>(sm);  // single mode: O of group 1, swizzled [128][D]
+      if (!pair) {
+        if (t == 1) {
+          *reinterpret_cast<float4*>(s_stat + row * 4) = make_float4(m, M, l, 0.f);
+#pragma unroll
+          for (int q = 0; q < D / 16; q++) {
+            uint32_t r16[16];
+            tmem_ld16(tO + q * 16, r16);
+            tmem_ld_wait();
+            if (steps > 0) {
+#pragma unroll
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<uint4*>(ex + row * D + (((q * 4 + (j >> 2)) ^ (row & 7)) << 2)) =
+                    make_uint4(r16[j], r16[j + 1], r16[j + 2], r16[j + 3]);
+            }
+          }
+        }
+        asm volatile("bar.sync 4, 256;" ::: "memory");
+        if (t == 0) {
+          const float4 s4 = *reinterpret_cast<const float4*>(s_stat + row * 4);
+          const float mt = fmaxf(m, s4.x), Mt = fmaxf(M, s4.y);
+          l = (m == -INFINITY ? l : l * ex2_ftz(m - mt)) + (s4.x == -INFINITY ? s4.z : s4.z * ex2_ftz(s4.x - mt));
+          mine = M == -INFINITY ? 0.f : ex2_ftz(M - Mt);
+          other = s4.y == -INFINITY ? 0.f : ex2_ftz(s4.y - Mt);
+          m = mt;
+          M = Mt;
+        }
+      }
+      if (pair || t == 0) {
+        float f = 1.f, lse = 0.f;
+        if (whole) {
+          f = finish_row(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
+          if (valid && p.a.lse) p.a.lse[orow] = lse;
+        } else {
+          *reinterpret_cast<float4*>(pp + irow * 4) = make_float4(m, M, l, 0.f);
+        }
+#pragma unroll
+        for (int q = 0; q < D / 16; q++) {
+          uint32_t r16[16];
+          tmem_ld16(tO + q * 16, r16);
+          tmem_ld_wait();
+          float x[16];
+#pragma unroll
+          for (int j = 0; j < 16; j++) x[j] = mine == 0.f ? 0.f : __uint_as_float(r16[j]) * mine;
+          if (other != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(ex + row * D + (((q * 4 + (j >> 2)) ^ (row & 7)) << 2));
+              x[j] = fmaf(y.x, other, x[j]);
+              x[j + 1] = fmaf(y.y, other, x[j + 1]);
+              x[j + 2] = fmaf(y.z, other, x[j + 2]);
+              x[j + 3] = fmaf(y.w, other, x[j + 3]);
+            }
+          }
+          if (whole) {
+            if (valid) {
+              uint32_t h[8];
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) h[j >> 1] = f == 0.f ? 0u : bf16x2_of(x[j] * f, x[j + 1] * f);
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + q * 16);
+              dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+              dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+              *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)irow * D + q * 16 + j) =
+                  make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+          }
+        }
+      }
+      // O is read and the exchange buffer is free before the next item's Q
+      tc_fence_before();
+      if (!pair) asm volatile("bar.sync 4, 256;" ::: "memory");
+      rg += n;
+      step += steps;
+    } while (walk_next(p, w));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D, bool SHARED>
+hcl_status_t launch_t(const Params& p, cudaStream_t st) {
+  auto kern = paged_tile_kernel<D, SHARED>;
+  const int smem = (int)Cfg<D, SHARED>::TOTAL + 1024;
+  static_assert(Cfg<D, SHARED>::TOTAL + 1024 <= 232448, "shared memory");
+  hcl_status_t e = set_kernel_attrs(reinterpret_cast<const void*>(kern), smem, false);
+  if (e != HCL_OK) return e;
+  return check_cuda(launch_pdl(kern, dim3(p.n_blocks), dim3(THREADS), (size_t)smem, st, 1, p),
+                    "paged attention (tiles) launch");
+}
+
+}  // namespace
+
+int tile_blocks() { return std::min(1024, num_sms()); }
+
+size_t tile_workspace(int d) { return (size_t)tile_blocks() * (2 * part_floats(ITEM, d) * 4 + 2 * sizeof(int4)); }
+
+hcl_status_t launch_tiles(const Params& p, cudaStream_t st) {
+  if (p.a.kv.d == 128) return p.a.kv.v ? launch_t<128, false>(p, st) : launch_t<128, true>(p, st);
+  return p.a.kv.v ? launch_t<64, false>(p, st) : launch_t<64, true>(p, st);
+}
+
+}  // namespace paged
+}  // namespace hcl
