@@ -40,15 +40,29 @@ constexpr int ROWS_ITEM = 256;     // query rows of an item of the tile kernel
 // A partial result: (m, M, l, -) of each row, then O of each row.
 __host__ __device__ constexpr size_t part_floats(int rows, int d) { return rows * 4 + rows * (size_t)d; }
 
+// n / d for 0 <= n < 2^31 by a multiplication: q = (n * mul >> 32 + n) >> shift.
+struct FastDiv {
+  uint32_t mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    shift = 0;
+    while ((1u << shift) < d) shift++;
+    mul = uint32_t((uint64_t(1) << 32) * ((uint64_t(1) << shift) - d) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return int((__umulhi(uint32_t(n), mul) + uint32_t(n)) >> shift);
+  }
+};
+
 struct Params {
   PagedAttnArgs a;
+  FastDiv by_G, by_m;
   int sh;            // log2(page)
   int G;             // query heads per KV head
   float scale2;      // scale * log2(e)
   int n_blocks;      // blocks that share the units
   float* part;       // partial results
-  int4* meta;        // two per block: its first unit, the first unit of the item it falls into (64 bits
-                     // each), then request, KV head, whether a split item ends here, its first query row
+  struct Meta* meta; // one per block
   long long limit;
 };
 
@@ -61,10 +75,9 @@ struct Req {
 
 // Row range [lo, hi) that query i of a request sees.
 __device__ __forceinline__ int vis_hi(const Params& p, const Req& r, int i) {
-  const long long pos = (long long)r.qs + i;
-  if (pos < 0) return 0;
-  const long long h = p.a.m == 1 ? pos + 1 : (pos + 1) / p.a.m;
-  return (int)min((long long)r.len, h);
+  const long long n = (long long)r.qs + i + 1;  // positions up to the query's
+  if (n <= 0) return 0;
+  return min(r.len, p.by_m.div((int)min(n, 0x7FFFFFFFll)));
 }
 __device__ __forceinline__ int vis_lo(const Params& p, const Req& r, int i) {
   if (p.a.W == 0) return 0;
@@ -93,19 +106,21 @@ __device__ __forceinline__ Req load_req(const Params& p, int b, bool say) {
   return r;
 }
 
-// This block's share of the units.  units(b): those of request b.  Every thread of the block
-// calls it (NT threads, a multiple of 32); s: scratch of NT / 32 + 4 words.
+// This block's share of the units of n entries (requests, or tiles of requests): units(e) of
+// entry e, each asked for by one thread, e ascending.  No more blocks take part than there are
+// units.  Every thread of the block calls it (NT threads, a multiple of 32); s: scratch of
+// NT / 32 + 4 words.
 struct Share {
   long long u0, u1;  // units [u0, u1)
-  int b;             // the request of u0
-  long long rem;     // u0's place among that request's units
+  long long tot;     // all units
+  int nb;            // blocks that have any
+  int e;             // the entry of u0
+  long long rem;     // u0's place among that entry's units
 };
-template <int NT, typename F>
-__device__ __forceinline__ Share find_share(int B, int block, int n_blocks, long long* s, F units) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (B + NT - 1) / NT, b0 = min(B, tid * per), b1 = min(B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; b++) mine += units(b);
+// Sum of the threads' values before this thread, and of all.
+template <int NT>
+__device__ __forceinline__ long long block_prefix(long long mine, long long* s, long long* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -115,30 +130,53 @@ __device__ __forceinline__ Share find_share(int B, int block, int n_blocks, long
   if (lane == 31) s[warp] = inc;
   __syncthreads();
   long long off = 0, tot = 0;
+#pragma unroll
   for (int w = 0; w < NT / 32; w++) {
-    if (w < warp) off += s[w];
-    tot += s[w];
+    const long long x = s[w];
+    if (w < warp) off += x;
+    tot += x;
   }
+  *total = tot;
+  return off + inc - mine;
+}
+template <int NT, typename F>
+__device__ __forceinline__ Share find_share(int n, int block, int n_blocks, long long* s, F units) {
+  const int tid = threadIdx.x, per = (n + NT - 1) / NT, e0 = min(n, tid * per), e1 = min(n, e0 + per);
+  long long mine = 0;
+  for (int e = e0; e < e1; e++) mine += units(e);
   Share r;
-  r.u0 = tot * block / n_blocks;
-  r.u1 = tot * (block + 1) / n_blocks;
-  long long at = off + inc - mine;
-  if (r.u0 < tot && at <= r.u0 && r.u0 < at + mine) {
-    for (int b = b0; b < b1; b++) {
-      const long long u = units(b);
-      if (r.u0 < at + u) {
-        s[NT / 32] = b;
-        s[NT / 32 + 1] = r.u0 - at;
-        break;
+  long long at = block_prefix<NT>(mine, s, &r.tot);
+  r.nb = (int)min((long long)n_blocks, r.tot);
+  r.u0 = r.u1 = 0;
+  if (block < r.nb) {
+    r.u0 = r.tot * block / r.nb;
+    r.u1 = r.tot * (block + 1) / r.nb;
+    if (at <= r.u0 && r.u0 < at + mine) {
+      for (int e = e0; e < e1; e++) {
+        const long long u = units(e);
+        if (r.u0 < at + u) {
+          s[NT / 32] = e;
+          s[NT / 32 + 1] = r.u0 - at;
+          break;
+        }
+        at += u;
       }
-      at += u;
     }
   }
   __syncthreads();
-  r.b = (int)s[NT / 32];
+  r.e = (int)s[NT / 32];
   r.rem = s[NT / 32 + 1];
   return r;
 }
+
+// What the merge needs of a block: whether a request that an earlier block began ends in it
+// (then that item's first unit, all units, request, KV head and first query row).
+struct Meta {
+  long long first, tot;
+  int ends, b, g, row0;
+  int nb, pad[3];
+};
+static_assert(sizeof(Meta) == 48, "Meta");
 
 // log2 of a page scale (exact for powers of two), the scale not below 2^-126.
 __device__ __forceinline__ float log2_scale(float s) {
@@ -208,9 +246,13 @@ hcl_status_t launch_rows(const Params& p, cudaStream_t st);
 hcl_status_t launch_tiles(const Params& p, cudaStream_t st);
 int rows_blocks();
 int tile_blocks();
-size_t rows_workspace(int d);
-size_t tile_workspace(int d);
 hcl_status_t launch_merge(const Params& p, int rows, cudaStream_t st);
+// Workspace of a kernel with n blocks and items of `rows` rows: the blocks' Meta, then two parts
+// each.
+constexpr size_t meta_bytes(int n) { return (size_t(n) * 48 + 127) / 128 * 128; }
+constexpr size_t split_workspace(int n, int rows, int d) {
+  return meta_bytes(n) + 2 * size_t(n) * part_floats(rows, d) * 4;
+}
 // Tensor map of a code plane as rows of d bytes, boxes of `rows` rows.
 hcl_status_t code_map(CUtensorMap* m, const void* codes, const hcl_paged_kv_t& kv, int rows, bool swizzle);
 

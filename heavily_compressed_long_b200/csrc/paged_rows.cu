@@ -89,7 +89,7 @@ __device__ __forceinline__ void walk_set(const Params& p, Walk& w) {
 __device__ __forceinline__ bool walk_first(const Params& p, const Share& s, Walk& w) {
   w.left = s.u1 - s.u0;
   if (w.left <= 0) return false;
-  w.b = s.b;
+  w.b = s.e;
   w.r = load_req(p, w.b, false);
   w.nt = tiles_of(p, w.r, &w.t0);
   w.g = (int)(s.rem / w.nt);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     paged_rows_kernel(const Params p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = Cfg<D, SHARED>;
   extern __shared__ __align__(1024) uint8_t raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset: the compiler still sees shared memory)
   float* s_scale = reinterpret_cast<float*>(sm + C::SCALES);
   float* s_merge = reinterpret_cast<float*>(sm + C::MERGE);
   float* s_stat = reinterpret_cast<float*>(sm + C::STATS);
@@ -141,17 +141,17 @@ __global__ void __launch_bounds__(THREADS, 2)
                                             int t0;
                                             return (long long)tiles_of(p, r, &t0) * p.a.kv.Hkv;
                                           });
-  Walk w;
+  Walk w = {};
   const bool any = walk_first(p, share, w);
   if (tid == 0) {
-    // for the merge: this block's first unit and the first unit of the item it falls into
-    long long* m = reinterpret_cast<long long*>(p.meta + 2 * blockIdx.x);
-    m[0] = share.u0;
-    m[1] = any ? share.u0 - w.tile : share.u0;
-    reinterpret_cast<int*>(m)[4] = any ? w.b : -1;
-    reinterpret_cast<int*>(m)[5] = any ? w.g : 0;
-    reinterpret_cast<int*>(m)[6] = any && w.tile > 0 && w.tile + w.count == w.nt;  // a split item ends here
-    reinterpret_cast<int*>(m)[7] = 0;                                              // its first query row
+    Meta* m = p.meta + blockIdx.x;
+    m->ends = any && w.tile > 0 && w.tile + w.count == w.nt;
+    m->first = share.u0 - w.tile;
+    m->tot = share.tot;
+    m->nb = share.nb;
+    m->b = w.b;
+    m->g = w.g;
+    m->row0 = 0;
   }
   if (!any) return;
 
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int h = 0; h < 2; h++) {
       const int row = r0 + 8 * h;
       const bool valid = row < nrows;
-      const int i = valid ? row / p.G : 0, head = w.g * p.G + (valid ? row % p.G : 0);
+      const int i = valid ? p.by_G.div(row) : 0, head = w.g * p.G + (valid ? row - i * p.G : 0);
       hi_r[h] = valid ? vis_hi(p, w.r, i) : 0;
       lo_r[h] = valid ? vis_lo(p, w.r, i) : 0;
       const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.q) +
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       for (int h = 0; h < 2; h++) {
         const int row = r0 + 8 * h;
         const bool valid = row < nrows;
-        const int i = valid ? row / p.G : 0, head = w.g * p.G + (valid ? row % p.G : 0);
+        const int i = valid ? p.by_G.div(row) : 0, head = w.g * p.G + (valid ? row - i * p.G : 0);
         const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
         float f = 1.f, lse = 0.f;
         float* pp = p.part + (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * part_floats(ROWS_SMALL, D);
@@ -508,8 +508,6 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
 }  // namespace
 
 int rows_blocks() { return std::min(1024, 2 * num_sms()); }
-
-size_t rows_workspace(int d) { return 2 * (size_t)rows_blocks() * (part_floats(ROWS_SMALL, d) * 4 + sizeof(int4)); }
 
 hcl_status_t launch_rows(const Params& p, cudaStream_t st) {
   if (p.a.kv.d == 128) return p.a.kv.v ? launch_t<128, false>(p, st) : launch_t<128, true>(p, st);

@@ -9,6 +9,7 @@
 //                     registers) to fp16 tiles in shared memory, 128-byte swizzle.  The same
 //                     layout serves K (K-major B operand of S = Q K^T) and V (MN-major B operand
 //                     of O += P V); rows that are both key and value are widened once.
+//   warp 13           one thread walks the block's items and describes them, up to four ahead
 //   warp 12           one thread issues every MMA:  PV_0(r), S_0(r+1), PV_1(r), S_1(r+1), so one
 //                     tile's softmax runs under the other tile's MMAs
 // P (fp16) is written over the first half of its S in tensor memory and read there as the A
@@ -29,34 +30,16 @@ namespace {
 
 constexpr int TILE = 128;      // KV rows per round, query rows per tile
 constexpr int ITEM = ROWS_ITEM;  // query rows per item
-constexpr int THREADS = 13 * 32;
+constexpr int THREADS = 16 * 32;  // warps 14, 15 idle (registers are handed out by fours of warps)
 constexpr int PRING = 8;       // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
 struct RoundPar {              // what the softmax needs of a round's pages (groups of 16 rows)
-  float kc[8], lv[8], wl[8];
+  float kc[8], lv[8], wl[8];   // scale2 * k_scale, log2(v_scale), 2^(lvref - lv)
   uint32_t valid[4], poison[4];
   float lvref;
-  float pad[7];
-};
-
-template <int D, bool SHARED>
-struct Cfg {
-  static constexpr int PIECES = D / 16;               // 16-code pieces of a row
-  static constexpr int RPP = 128 / PIECES;            // rows per pass of the widening threads
-  static constexpr int PASSES = TILE / RPP;
-  static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile, and of a K or V tile
-  static constexpr int NK = SHARED ? 4 : 2;           // K (or shared) tiles in the ring
-  static constexpr int NV = SHARED ? 4 : 2;
-  static constexpr uint32_t K = 2 * QT;
-  static constexpr uint32_t V = SHARED ? K : K + NK * QT;
-  static constexpr uint32_t PAR = K + 4 * QT;
-  static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
-  static constexpr uint32_t BAR = STAT + 128 * 16;
-  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 2 + 2 + 1;
-  static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
-  static constexpr uint32_t MISC = SCRATCH + (13 + 4) * 8;
-  static constexpr uint32_t TOTAL = MISC + 16;
+  uint32_t edge;               // some query row of the item does not see the round whole
+  float pad[6];
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
@@ -96,7 +79,7 @@ __device__ __forceinline__ int tiles_of(const Params& p, const Req& r) {
 }
 // Rounds of a tile: first KV row (a multiple of TILE) and how many (at least one).
 __device__ __forceinline__ int rounds_of(const Params& p, const Req& r, int tile, int* j0) {
-  const int i0 = tile * ITEM / p.G, i1 = (min(r.nq * p.G, (tile + 1) * ITEM) - 1) / p.G;
+  const int i0 = p.by_G.div(tile * ITEM), i1 = p.by_G.div(min(r.nq * p.G, (tile + 1) * ITEM) - 1);
   const int hi = vis_hi(p, r, i1), lo = min(vis_lo(p, r, i0), hi);
   *j0 = 0;
   if (hi <= lo) return 1;
@@ -104,6 +87,7 @@ __device__ __forceinline__ int rounds_of(const Params& p, const Req& r, int tile
   return (hi - *j0 + TILE - 1) / TILE;
 }
 
+// Items in order: request, tile, KV head.
 struct Walk {
   Req r;
   int b, g, tile, j0, nt;  // request, KV head, tile; its first KV row and rounds
@@ -114,51 +98,72 @@ __device__ __forceinline__ void walk_set(const Params& p, Walk& w) {
   w.count = (int)min((long long)(w.nt - w.rd), w.left);
   w.left -= w.count;
 }
-__device__ __forceinline__ bool walk_first(const Params& p, const Share& s, Walk& w) {
+__device__ __forceinline__ bool walk_first(const Params& p, const Share& s, int b, int tile, Walk& w) {
   w.left = s.u1 - s.u0;
   if (w.left <= 0) return false;
-  w.b = s.b;
-  w.r = load_req(p, w.b, false);
-  const int nt = tiles_of(p, w.r);
-  int per = 0, j0;
-  for (int t = 0; t < nt; t++) per += rounds_of(p, w.r, t, &j0);
-  w.g = (int)(s.rem / per);
-  int rem = (int)(s.rem % per);
-  w.tile = 0;
-  while (true) {
-    w.nt = rounds_of(p, w.r, w.tile, &w.j0);
-    if (rem < w.nt) break;
-    rem -= w.nt;
-    w.tile++;
-  }
-  w.rd = rem;
+  w.b = b;
+  w.tile = tile;
+  w.r = load_req(p, b, false);
+  w.nt = rounds_of(p, w.r, tile, &w.j0);
+  w.g = (int)s.rem / w.nt;
+  w.rd = (int)s.rem - w.g * w.nt;
   walk_set(p, w);
   return true;
 }
 __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
   if (w.left <= 0) return false;
-  if (++w.tile == tiles_of(p, w.r)) {
-    w.tile = 0;
-    if (++w.g == p.a.kv.Hkv) {
-      w.g = 0;
+  if (++w.g == p.a.kv.Hkv) {
+    w.g = 0;
+    if (++w.tile == tiles_of(p, w.r)) {
+      w.tile = 0;
       do w.r = load_req(p, ++w.b, false);
       while (tiles_of(p, w.r) == 0);
     }
+    w.nt = rounds_of(p, w.r, w.tile, &w.j0);
   }
-  w.nt = rounds_of(p, w.r, w.tile, &w.j0);
   w.rd = 0;
   walk_set(p, w);
   return true;
 }
-__device__ __forceinline__ int item_rows(const Params& p, const Walk& w) {
-  return min(ITEM, w.r.nq * p.G - w.tile * ITEM);
-}
+// What the roles are told of an item, in shared memory, written by the walking warp.
+struct Item {
+  int count;               // rounds of this block's part; 0: no item more
+  int rows;                // query rows (> 128: both tiles)
+  int j0;                  // first KV row of the part
+  int b, g;                // request, KV head
+  int row0, c0;            // first query row within the request, the request's first row of q
+  int qs, len;             // position of its first query, rows held
+  int any_hi, all_lo, all_hi;  // some row sees KV rows below any_hi; all see [all_lo, all_hi)
+  int whole, head;         // not split; the part begins inside the item (an earlier block has its front)
+  int pad[2];
+};
+constexpr int IRING = 4;
+
+template <int D, bool SHARED>
+struct Cfg {
+  static constexpr int PIECES = D / 16;               // 16-code pieces of a row
+  static constexpr int RPP = 128 / PIECES;            // rows per pass of the widening threads
+  static constexpr int PASSES = TILE / RPP;
+  static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile, and of a K or V tile
+  static constexpr int NK = SHARED ? 4 : 2;           // K (or shared) tiles in the ring
+  static constexpr int NV = SHARED ? 4 : 2;
+  static constexpr uint32_t K = 2 * QT;
+  static constexpr uint32_t V = SHARED ? K : K + NK * QT;
+  static constexpr uint32_t PAR = K + 4 * QT;
+  static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
+  static constexpr uint32_t ITEMS = STAT + 128 * 16;
+  static constexpr uint32_t BAR = ITEMS + IRING * sizeof(Item);
+  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 2 + 2 + 1 + 2 * IRING;
+  static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
+  static constexpr uint32_t MISC = SCRATCH + (16 + 4) * 8;
+  static constexpr uint32_t TOTAL = MISC + 16;
+};
 
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) {
   using C = Cfg<D, SHARED>;
   extern __shared__ __align__(1024) uint8_t raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset: the compiler still sees shared memory)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RoundPar* par = reinterpret_cast<RoundPar*>(sm + C::PAR);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + C::BAR);
@@ -170,6 +175,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
   uint64_t* o_done = s_full + 4;       // [2] PV of the step completed
   uint64_t* q_full = s_full + 6;       // [2] Q tile in shared memory
   uint64_t* drain = s_full + 8;
+  uint64_t* i_full = s_full + 9;             // [IRING] an item's description stands
+  uint64_t* i_empty = i_full + IRING;        // [IRING] every role is done with it
+  Item* items = reinterpret_cast<Item*>(sm + C::ITEMS);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + C::MISC + 4);
   if (tid == 0) {
@@ -182,6 +190,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       mbar_init(&q_full[t], 128);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < IRING; i++) { mbar_init(&i_full[i], 1); mbar_init(&i_empty[i], 128 + 256 + 1); }
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -191,42 +200,69 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
   }
   pdl_enter();
   tc_fence_before();
-  const Share share = find_share<THREADS>(p.a.B, blockIdx.x, p.n_blocks, reinterpret_cast<long long*>(sm + C::SCRATCH),
-                                          [&](int b) {
-                                            const Req r = load_req(p, b, blockIdx.x == 0);
-                                            const int nt = tiles_of(p, r);
-                                            long long n = 0;
-                                            int j0;
-                                            for (int t = 0; t < nt; t++) n += rounds_of(p, r, t, &j0);
-                                            return n * p.a.kv.Hkv;
-                                          });
+  // Units are rounds; the entries that share them are all tiles of all requests, so that no
+  // thread has a long prompt to itself.  s_first (in memory that Q will take): each request's
+  // first tile.
+  long long* scratch = reinterpret_cast<long long*>(sm + C::SCRATCH);
+  int* s_first = reinterpret_cast<int*>(sm);
+  const int per = (p.a.B + THREADS - 1) / THREADS;
+  const int b_lo = min(p.a.B, tid * per), b_hi = min(p.a.B, b_lo + per);
+  long long tiles = 0, all_tiles;
+  for (int b = b_lo; b < b_hi; b++) tiles += tiles_of(p, load_req(p, b, blockIdx.x == 0));
+  tiles = block_prefix<THREADS>(tiles, scratch, &all_tiles);
+  for (int b = b_lo; b < b_hi; b++) {
+    s_first[b] = (int)tiles;
+    tiles += tiles_of(p, load_req(p, b, false));
+  }
+  __syncthreads();
+  int at_b = -1, at_end = 0;  // the request of the thread's current tile, and the tile after its last
+  Req at_r = {};
+  auto tile_at = [&](int e) {  // request of tile e
+    if (at_b < 0 || e >= at_end || e < s_first[at_b]) {
+      int lo = 0, hi = p.a.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_first[mid] <= e) lo = mid;
+        else hi = mid;
+      }
+      at_b = lo;
+      at_r = load_req(p, lo, false);
+      at_end = s_first[lo] + tiles_of(p, at_r);
+    }
+    return at_b;
+  };
+  const Share share = find_share<THREADS>((int)all_tiles, blockIdx.x, p.n_blocks, scratch, [&](int e) {
+    int j0;
+    tile_at(e);
+    return (long long)rounds_of(p, at_r, e - s_first[at_b], &j0) * p.a.kv.Hkv;
+  });
+  at_b = -1;
+  const int b0 = share.u1 > share.u0 ? tile_at(share.e) : 0;
+  const int tile0 = share.u1 > share.u0 ? share.e - s_first[b0] : 0;
+  __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *s_tmem;
-  Walk w;
-  const bool any = walk_first(p, share, w);
-  if (tid == 0) {
-    long long* m = reinterpret_cast<long long*>(p.meta + 2 * blockIdx.x);
-    m[0] = share.u0;
-    m[1] = any ? share.u0 - w.rd : share.u0;
-    int* mi = reinterpret_cast<int*>(m);
-    mi[4] = any ? w.b : -1;
-    mi[5] = any ? w.g : 0;
-    mi[6] = any && w.rd > 0 && w.rd + w.count == w.nt;
-    mi[7] = any ? w.tile * ITEM : 0;
-  }
+  const bool any = share.u1 > share.u0;
+  if (!any && tid == 0) p.meta[blockIdx.x].ends = 0;
 
+  // registers of the four warpgroups: 152 + 152 + 120 + 88 = 4 * 128
   if (any && warp >= 8 && warp < 12) {
     // ------------------------------------------------------------------ widening
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
     const int wt = tid - 256, pc = wt % C::PIECES, pr = wt / C::PIECES;
     const uint8_t* kcodes = static_cast<const uint8_t*>(p.a.kv.k);
     const uint8_t* vcodes = static_cast<const uint8_t*>(p.a.kv.v);
     const int pmask = p.a.kv.page - 1;
     bool ok = true, fault = false;
     uint32_t rg = 0;  // rounds so far
-    do {
-      const int rows = item_rows(p, w), i0 = w.tile * ITEM / p.G, i1 = (w.tile * ITEM + rows - 1) / p.G;
-      const int all_lo = vis_lo(p, w.r, i1), all_hi = vis_hi(p, w.r, i0), any_hi = vis_hi(p, w.r, i1);
-      const int32_t* trow = p.a.table + (size_t)w.b * p.a.max_pages;
+    for (uint32_t it = 0;; it++) {
+      const Item* im = items + it % IRING;
+      ok = mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
+      ok = !bar_or(2, 128, !ok);
+      const int count = ok ? im->count : 0;
+      if (count == 0) break;
+      const int all_lo = im->all_lo, all_hi = im->all_hi, any_hi = im->any_hi, jfirst = im->j0, g = im->g;
+      const int32_t* trow = p.a.table + (size_t)im->b * p.a.max_pages;
       // page of KV row j: -2 where no row is wanted, -1 for an id outside the cache
       auto page_at = [&](int j) {
         int id = j < any_hi ? __ldg(trow + (j >> p.sh)) : -2;
@@ -235,16 +271,16 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       };
       auto load_ids = [&](int i, int (&id)[C::PASSES]) {
 #pragma unroll
-        for (int q = 0; q < C::PASSES; q++) id[q] = i < w.count ? page_at(w.j0 + (w.rd + i) * TILE + q * C::RPP + pr) : -2;
+        for (int q = 0; q < C::PASSES; q++) id[q] = i < count ? page_at(jfirst + i * TILE + q * C::RPP + pr) : -2;
       };
       auto load_codes = [&](const uint8_t* codes, int i, const int (&id)[C::PASSES], uint4 (&x)[C::PASSES]) {
 #pragma unroll
         for (int q = 0; q < C::PASSES; q++) {
-          const int j = w.j0 + (w.rd + i) * TILE + q * C::RPP + pr;
+          const int j = jfirst + i * TILE + q * C::RPP + pr;
           x[q] = make_uint4(0, 0, 0, 0);
           if (id[q] >= 0 && j < any_hi)
             x[q] = __ldg(reinterpret_cast<const uint4*>(
-                codes + ((((size_t)id[q] * p.a.kv.Hkv + w.g) << p.sh) + (j & pmask)) * D + pc * 16));
+                codes + ((((size_t)id[q] * p.a.kv.Hkv + g) << p.sh) + (j & pmask)) * D + pc * 16));
         }
       };
       auto store_tile = [&](uint8_t* tile, const uint4 (&x)[C::PASSES]) {
@@ -282,23 +318,28 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       load_ids(0, id);
       load_codes(kcodes, 0, id, kx);
       if constexpr (!SHARED) load_codes(vcodes, 0, id, vx);
+      load_ids(1, id);
       // page parameters: lane g8 of the first widening warp has group g8
-      int gid = -2;
+      int gid = -2, gid_next = -2;
       float gks = 0.f, gvs = 0.f, lvref = -INFINITY;
+      auto group_page = [&](int i) { return i < count ? page_at(jfirst + i * TILE + (lane & 7) * 16) : -2; };
       auto load_scales = [&](int i) {
-        const int j = w.j0 + (w.rd + i) * TILE + (lane & 7) * 16;
-        gid = i < w.count ? page_at(j) : -2;
+        gid = gid_next;
+        gid_next = group_page(i + 1);
         if (gid >= 0) {
-          const size_t pg = (size_t)gid * p.a.kv.Hkv + w.g;
+          const size_t pg = (size_t)gid * p.a.kv.Hkv + g;
           gks = __ldg(p.a.kv.k_scale + pg);
           gvs = SHARED ? gks : __ldg(p.a.kv.v_scale + pg);
         }
       };
-      if (warp == 8) load_scales(0);
-      for (int i = 0; i < w.count; i++, rg++) {
+      if (warp == 8) {
+        gid_next = group_page(0);
+        load_scales(0);
+      }
+      for (int i = 0; i < count; i++, rg++) {
         const int kb = rg % C::NK;
         RoundPar* rp = par + rg % PRING;
-        const int j0 = w.j0 + (w.rd + i) * TILE;
+        const int j0 = jfirst + i * TILE;
         const bool edge = j0 < all_lo || j0 + TILE > all_hi;
         uint64_t* ke = SHARED ? v_empty : k_empty;
         if (rg >= C::NK) ok = ok && mbar_wait(&ke[kb], ((rg / C::NK) & 1) ^ 1, p.limit, s_abort);
@@ -318,7 +359,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
               rp->valid[lane] = ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
               rp->poison[lane] = 0u;
             }
-            if (lane == 0) rp->lvref = lvref == -INFINITY ? 0.f : lvref;
+            if (lane == 0) {
+              rp->lvref = lvref == -INFINITY ? 0.f : lvref;
+              rp->edge = edge;
+            }
           }
         }
         // the parameters stand before any thread marks a poisoned row
@@ -327,9 +371,9 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
         store_tile(sm + C::K + kb * C::QT, kx);
         fence_proxy_async_smem();
         mbar_arrive(&k_full[kb]);
-        load_ids(i + 1, id);
         load_codes(kcodes, i + 1, id, kx);
         if (warp == 8) load_scales(i + 1);
+        if constexpr (SHARED) load_ids(i + 2, id);
         if constexpr (!SHARED) {
           const int vb = rg % C::NV;
           if (rg >= C::NV) ok = ok && mbar_wait(&v_empty[vb], ((rg / C::NV) & 1) ^ 1, p.limit, s_abort);
@@ -338,74 +382,94 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
           fence_proxy_async_smem();
           mbar_arrive(&v_full[vb]);
           load_codes(vcodes, i + 1, id, vx);
+          load_ids(i + 2, id);
         }
       }
       ok = !bar_or(2, 128, !ok);  // the four warps go on, or end, together
-    } while (ok && walk_next(p, w));
+      mbar_arrive(&i_empty[it % IRING]);
+      if (!ok) break;
+    }
     if (!ok) {
       *s_abort = 1;
       report(p.a.status, HCL_ERR_TIMEOUT);
     }
     if (fault) report(p.a.status, HCL_ERR_DEVICE_FAULT);
-  } else if (any && warp == 12) {
+  } else if (any && warp >= 12) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 12 && lane == 0) {
       const uint64_t dq = make_sdesc(smem_u32(sm), 16, 1024, SMEM_SWIZZLE_128B);
       const uint64_t dk = make_sdesc(smem_u32(sm + C::K), 16, 1024, SMEM_SWIZZLE_128B);
       const uint64_t dv = make_sdesc(smem_u32(sm + C::V), 16384, 1024, SMEM_SWIZZLE_128B);
       constexpr uint32_t idS = idesc_f16(128, TILE), idPV = idesc_f16(128, D) | (1u << 16);
-      uint32_t rg = 0, step[2] = {0, 0}, items = 0;
+      // rg: rounds before this item; par_t: parity of tile t's step count; qp: of the items
+      uint32_t rg = 0, par0 = 0, par1 = 0, qp = 0;
       bool ok = true;
-      do {
-        const int n = w.count;
-        const bool pair = item_rows(p, w) > 128;
-        const int steps[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
-        auto round_of = [&](int t, int k) { return rg + uint32_t(pair ? k : 2 * k + t); };
-        auto issue_s = [&](int t, int k) {
-          const uint32_t R = round_of(t, k), kb = R % C::NK;
-          ok = ok && mbar_wait(&k_full[kb], (R / C::NK) & 1, p.limit, s_abort);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t a0 = dq + uint64_t((pair ? t : 0) * (C::QT >> 4)), b0 = dk + uint64_t(kb * (C::QT >> 4));
+      // S of round R into tile t's scores, with the Q tile at aq
+      auto issue_s = [&](uint32_t R, int t, uint64_t aq, bool frees) {
+        const uint32_t kb = R % C::NK;
+        ok = ok && mbar_wait(&k_full[kb], (R / C::NK) & 1, p.limit, s_abort);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b0 = dk + uint64_t(kb * (C::QT >> 4));
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ks++) {
-            const uint32_t off = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
-            umma_bf16(tbase + t * TILE, a0 + off, b0 + off, idS, ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < D / 16; ks++) {
+          const uint32_t off = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
+          umma_bf16(tbase + t * TILE, aq + off, b0 + off, idS, ks > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[t]);
+        if (!SHARED && frees) umma_commit(&k_empty[kb]);
+      };
+      // O of tile t += P V of round R
+      auto issue_pv = [&](uint32_t R, int t, uint32_t parity, bool first, bool frees) {
+        const uint32_t vb = R % C::NV;
+        ok = ok && mbar_wait(&p_full[t], parity, p.limit, s_abort);
+        if (!SHARED) ok = ok && mbar_wait(&v_full[vb], (R / C::NV) & 1, p.limit, s_abort);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b0 = dv + uint64_t(vb * (C::QT >> 4));
+#pragma unroll
+        for (int ks = 0; ks < 8; ks++)
+          umma_f16_ta(tbase + O_COL + t * 128, tbase + t * TILE + ks * 8, b0 + uint32_t(ks * (2048 >> 4)), idPV,
+                      ks > 0 || !first ? 1u : 0u);
+        umma_commit(&o_done[t]);
+        if (frees) umma_commit(&v_empty[vb]);
+      };
+      for (uint32_t it = 0; ok; it++) {
+        ok = mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
+        const int n = ok ? items[it % IRING].count : 0;
+        if (n == 0) break;
+        const bool pair = items[it % IRING].rows > 128;
+        mbar_arrive(&i_empty[it % IRING]);
+        ok = ok && mbar_wait(&q_full[0], qp, p.limit, s_abort);
+        if (pair) ok = ok && mbar_wait(&q_full[1], qp, p.limit, s_abort);
+        // tile t's step k is round k (pair) or 2k + t (single)
+        const uint64_t aq1 = pair ? dq + uint64_t(C::QT >> 4) : dq;
+        const int n0 = pair ? n : (n + 1) / 2, n1 = pair ? n : n / 2;
+        const uint32_t stride = pair ? 1 : 2, shift = pair ? 0 : 1;
+        issue_s(rg, 0, dq, !pair);
+        if (n1 > 0) issue_s(rg + shift, 1, aq1, true);
+        uint32_t R = rg;
+        for (int k = 0; k < n0 && ok; k++, R += stride) {
+          issue_pv(R, 0, par0, k == 0, !pair);
+          if (k + 1 < n0) {
+            // S_t of the next step overwrites P_t: PV_t must have completed
+            ok = ok && mbar_wait(&o_done[0], par0, p.limit, s_abort);
+            issue_s(R + stride, 0, dq, !pair);
           }
-          umma_commit(&s_full[t]);
-          if (!SHARED && (!pair || t == 1)) umma_commit(&k_empty[kb]);
-        };
-        for (int t = 0; t < (pair ? 2 : 1) && ok; t++) ok = mbar_wait(&q_full[t], items & 1, p.limit, s_abort);
-        for (int t = 0; t < 2; t++)
-          if (steps[t] > 0) issue_s(t, 0);
-        for (int k = 0; k < steps[0] && ok; k++) {
-          for (int t = 0; t < 2 && ok; t++) {
-            if (k >= steps[t]) continue;
-            const uint32_t R = round_of(t, k), vb = R % C::NV;
-            ok = mbar_wait(&p_full[t], (step[t] + k) & 1, p.limit, s_abort);
-            if (ok && !SHARED) ok = mbar_wait(&v_full[vb], (R / C::NV) & 1, p.limit, s_abort);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t b0 = dv + uint64_t(vb * (C::QT >> 4));
-#pragma unroll
-            for (int ks = 0; ks < 8; ks++)
-              umma_f16_ta(tbase + O_COL + t * 128, tbase + t * TILE + ks * 8, b0 + uint32_t(ks * (2048 >> 4)), idPV,
-                          (k > 0 || ks > 0) ? 1u : 0u);
-            umma_commit(&o_done[t]);
-            if (!pair || t == 1) umma_commit(&v_empty[vb]);
-            if (k + 1 < steps[t]) {
-              // S_t of the next step overwrites P_t: PV_t must have completed
-              ok = mbar_wait(&o_done[t], (step[t] + k) & 1, p.limit, s_abort);
-              issue_s(t, k + 1);
+          par0 ^= 1;
+          if (k < n1) {
+            issue_pv(R + shift, 1, par1, k == 0, true);
+            if (k + 1 < n1) {
+              ok = ok && mbar_wait(&o_done[1], par1, p.limit, s_abort);
+              issue_s(R + stride + shift, 1, aq1, true);
             }
+            par1 ^= 1;
           }
         }
         rg += n;
-        step[0] += steps[0];
-        step[1] += steps[1];
-        // q_full[1] is used by pairs only; its phase is kept in step by an arrival of the softmax
-        items++;
-      } while (ok && walk_next(p, w));
+        qp ^= 1;  // (group 1 arrives on q_full[1] in single mode too)
+      }
       if (!ok) {
         *s_abort = 1;
         report(p.a.status, HCL_ERR_TIMEOUT);
@@ -414,27 +478,85 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       umma_commit(drain);
       if (!mbar_wait(drain, 0, p.limit, nullptr)) report(p.a.status, HCL_ERR_TIMEOUT);
     }
+    if (warp == 13 && lane == 0) {
+      // ---------------------------------------------------------------- the items
+      Walk w;
+      bool more = walk_first(p, share, b0, tile0, w), ok = true;
+      Meta* m = p.meta + blockIdx.x;
+      m->ends = w.rd > 0 && w.rd + w.count == w.nt;
+      m->first = share.u0 - w.rd;
+      m->tot = share.tot;
+      m->nb = share.nb;
+      m->b = w.b;
+      m->g = w.g;
+      m->row0 = w.tile * ITEM;
+      for (uint32_t it = 0; ok; it++) {
+        if (it >= IRING) ok = mbar_wait(&i_empty[it % IRING], ((it / IRING) & 1) ^ 1, p.limit, s_abort);
+        if (!ok) break;
+        Item im = {};
+        if (more) {
+          im.count = w.count;
+          im.rows = min(ITEM, w.r.nq * p.G - w.tile * ITEM);
+          im.j0 = w.j0 + w.rd * TILE;
+          im.b = w.b;
+          im.g = w.g;
+          im.row0 = w.tile * ITEM;
+          im.c0 = w.r.c0;
+          im.qs = w.r.qs;
+          im.len = w.r.len;
+          const int i0 = p.by_G.div(im.row0), i1 = p.by_G.div(im.row0 + im.rows - 1);
+          im.any_hi = vis_hi(p, w.r, i1);
+          im.all_lo = vis_lo(p, w.r, i1);
+          im.all_hi = vis_hi(p, w.r, i0);
+          im.whole = w.count == w.nt;
+          im.head = w.rd > 0;
+        }
+        items[it % IRING] = im;
+        mbar_arrive(&i_full[it % IRING]);
+        if (!more) break;
+        more = walk_next(p, w);
+      }
+      if (!ok) {
+        *s_abort = 1;
+        report(p.a.status, HCL_ERR_TIMEOUT);
+      }
+    }
     __syncwarp();
   } else if (any && warp < 8) {
     // ------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lq = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tbase + lq + t * TILE, tO = tbase + lq + O_COL + t * 128;
     float* s_stat = reinterpret_cast<float*>(sm + C::STAT);
     uint32_t rg = 0, step = 0;
     bool ok = true;
-    do {
-      const int n = w.count, rows = item_rows(p, w);
+    for (uint32_t it = 0;; it++) {
+      const Item* im = items + it % IRING;
+      ok = mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
+      if (bar_or(3, 256, !ok)) { ok = false; break; }
+      const int n = im->count, rows = im->rows, jfirst = im->j0;
+      if (n == 0) break;
       const bool pair = rows > 128;
       const int irow = (pair ? t * 128 : 0) + row;  // row of the item
       const bool valid = irow < rows;
-      const int qr = w.tile * ITEM + (valid ? irow : 0), qi = qr / p.G, head = w.g * p.G + qr % p.G;
-      const int hi = valid ? vis_hi(p, w.r, qi) : 0, lo = valid ? vis_lo(p, w.r, qi) : 0;
+      int hi, lo;
+      size_t orow;
+      int head;
+      const __nv_bfloat16* qrow;
+      {
+        const int qr = im->row0 + (valid ? irow : 0), qi = p.by_G.div(qr);
+        const Req r = {0, im->c0, im->len, im->qs};
+        hi = valid ? vis_hi(p, r, qi) : 0;
+        lo = valid ? vis_lo(p, r, qi) : 0;
+        head = im->g * p.G + qr - qi * p.G;
+        orow = (size_t)(r.c0 + qi) * p.a.H + head;
+        qrow = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(r.c0 + qi) * p.a.q_stride + head * D;
+      }
       // Q row -> fp16 with its exponent taken out (in single mode group 1 only needs the factor)
       float back;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
-                                                          (int64_t)(w.r.c0 + qi) * p.a.q_stride + head * D);
+        const uint4* src = reinterpret_cast<const uint4*>(qrow);
         uint4 x[D / 8];
         float am = 0.f;
 #pragma unroll
@@ -466,6 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       bool sick = false;  // a NaN value in a row that this query sees
       auto look = [&](uint32_t R, int j0) {
         const RoundPar* rp = par + R % PRING;
+        if (!rp->edge) return;
 #pragma unroll
         for (int v = 0; v < 4; v++)
           if (rp->poison[v] & range_mask(j0 + 32 * v, lo, hi)) sick = true;
@@ -473,7 +596,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       for (int k = 0; k < steps; k++) {
         const int rr = pair ? k : 2 * k + t;
         const uint32_t R = rg + rr;
-        const int j0 = w.j0 + (w.rd + rr) * TILE;
+        const int j0 = jfirst + rr * TILE;
         ok = mbar_wait(&s_full[t], (step + k) & 1, p.limit, s_abort);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
@@ -483,29 +606,32 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
         uint32_t vb[4];
 #pragma unroll
         for (int v = 0; v < 4; v++) vb[v] = range_mask(j0 + 32 * v, lo, hi) & rp->valid[v];
+        const bool clear = (vb[0] & vb[1] & vb[2] & vb[3]) == 0xFFFFFFFFu;
+        // scores of columns 64 c .. 64 c + 63, -inf where this row sees nothing
         uint32_t sv[64];
+        auto load_scores = [&](int c) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) tmem_ld16(tS + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
+          tmem_ld_wait();
+          if (!clear) {
+#pragma unroll
+            for (int j = 0; j < 64; j++)
+              if (!((vb[2 * c + (j >> 5)] >> (j & 31)) & 1u)) sv[j] = 0xFF800000u;
+          }
+        };
         float mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++) {
-#pragma unroll
-          for (int q = 0; q < 4; q++) tmem_ld16(tS + hf * 64 + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
-          tmem_ld_wait();
+        for (int c = 1; c >= 0; c--) {
+          load_scores(c);
 #pragma unroll
           for (int q = 0; q < 4; q++) {
-            const uint32_t bits = (vb[2 * hf + (q >> 1)] >> (16 * (q & 1))) & 0xFFFFu;
-            float sx = -INFINITY;
-            if (bits == 0xFFFFu) {
+            float sx = fmaxf(__uint_as_float(sv[16 * q]), __uint_as_float(sv[16 * q + 1]));
 #pragma unroll
-              for (int j = 0; j < 16; j += 2)
-                sx = fmax3(sx, __uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1]));
-            } else if (bits != 0u) {
-#pragma unroll
-              for (int j = 0; j < 16; j++)
-                if ((bits >> j) & 1u) sx = fmaxf(sx, __uint_as_float(sv[16 * q + j]));
-            }
-            const float zx = sx == -INFINITY ? -INFINITY : sx * fmaxf(rp->kc[4 * hf + q] * back, SCALE_MIN);
+            for (int j = 2; j < 16; j += 2)
+              sx = fmax3(sx, __uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1]));
+            const float zx = sx * fmaxf(rp->kc[4 * c + q] * back, SCALE_MIN);
             mz = fmaxf(mz, zx);
-            mw = fmaxf(mw, zx + rp->lv[4 * hf + q]);
+            mw = fmaxf(mw, zx + rp->lv[4 * c + q]);
           }
         }
         const float m2 = fmaxf(m, mz);
@@ -527,36 +653,34 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
           }
         }
         const float Mu = M == -INFINITY ? 0.f : M, mu = m == -INFINITY ? 0.f : m;
-        // P over S: columns 64c .. 64c + 63 go to columns 32c .. 32c + 31, already read
+        // P over the first half of S: columns 64 c .. + 63 go to columns 32 c .. + 31, whose scores
+        // are in registers (c = 0) or used (c = 1)
         float lr = 0.f;
 #pragma unroll
         for (int c = 0; c < 2; c++) {
+          if (c == 1) load_scores(1);
 #pragma unroll
-          for (int q = 0; q < 4; q++) tmem_ld16(tS + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
-          tmem_ld_wait();
-          uint32_t pk[32];
+          for (int hf = 0; hf < 2; hf++) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            const uint32_t bits = (vb[2 * c + (q >> 1)] >> (16 * (q & 1))) & 0xFFFFu;
-            const float cc = fmaxf(rp->kc[4 * c + q] * back, SCALE_MIN), add = rp->lv[4 * c + q] - Mu + P_OFF;
-            const unsigned long long c2 = f2_make(cc, cc), a2 = f2_make(add, add);
-            unsigned long long g = 0ull;
+            for (int q = 0; q < 2; q++) {
+              const int gq = 4 * c + 2 * hf + q;
+              const float cc = fmaxf(rp->kc[gq] * back, SCALE_MIN), add = rp->lv[gq] - Mu + P_OFF;
+              const unsigned long long c2 = f2_make(cc, cc), a2 = f2_make(add, add);
+              unsigned long long g = 0ull;
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const unsigned long long x = f2_fma(
-                  f2_make(__uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1])), c2, a2);
-              float e0 = ex2_ftz(f2_lo(x)), e1 = ex2_ftz(f2_hi(x));
-              if (bits != 0xFFFFu) {
-                e0 = (bits >> j) & 1u ? e0 : 0.f;
-                e1 = (bits >> (j + 1)) & 1u ? e1 : 0.f;
+              for (int j = 0; j < 16; j += 2) {
+                const int e = 32 * hf + 16 * q + j;
+                const unsigned long long x =
+                    f2_fma(f2_make(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, a2);
+                const float e0 = ex2_ftz(f2_lo(x)), e1 = ex2_ftz(f2_hi(x));
+                g = f2_add(g, f2_make(e0, e1));
+                pk[8 * q + (j >> 1)] = half2_of(e0, e1);
               }
-              g = f2_add(g, f2_make(e0, e1));
-              pk[8 * q + (j >> 1)] = half2_of(e0, e1);
+              lr = fmaf(f2_lo(g) + f2_hi(g), rp->wl[gq], lr);
             }
-            lr = fmaf(f2_lo(g) + f2_hi(g), rp->wl[4 * c + q], lr);
+            tmem_st16(tS + 32 * c + 16 * hf, pk);
           }
-          tmem_st16(tS + 32 * c, *reinterpret_cast<const uint32_t(*)[16]>(&pk[0]));
-          tmem_st16(tS + 32 * c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16]));
         }
         l = fmaf(lr, ex2_ftz(Mu - P_OFF - rp->lvref - mu), l);
         tmem_st_wait();
@@ -568,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         if (ok) look(rg + (pair ? n - 1 : 2 * (steps - 1) + t),
-                     w.j0 + (w.rd + (pair ? n - 1 : 2 * (steps - 1) + t)) * TILE);
+                     jfirst + (pair ? n - 1 : 2 * (steps - 1) + t) * TILE);
       }
       if (sick) l = NAN;
       if (!ok) {
@@ -577,9 +701,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       }
       // both groups are done with their MMAs (Q's shared memory is free), or the block ends here
       if (bar_or(3, 256, !ok)) { ok = false; break; }
-      const bool whole = w.count == w.nt;
-      const size_t orow = (size_t)(w.r.c0 + qi) * p.a.H + head;
-      float* pp = p.part + (2 * (size_t)blockIdx.x + (w.rd == 0 ? 1 : 0)) * part_floats(ITEM, D);
+      const bool whole = im->whole != 0;
+      float* pp = p.part + (2 * (size_t)blockIdx.x + (im->head ? 0 : 1)) * part_floats(ITEM, D);
       float mine = 1.f, other = 0.f;  // factors of this group's O and, in single mode, group 1's
       float* ex = reinterpret_cast<float*>(sm);  // single mode: O of group 1, swizzled [128][D]
       if (!pair) {
@@ -655,9 +778,10 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       // O is read and the exchange buffer is free before the next item's Q
       tc_fence_before();
       if (!pair) asm volatile("bar.sync 4, 256;" ::: "memory");
+      mbar_arrive(&i_empty[it % IRING]);
       rg += n;
       step += steps;
-    } while (walk_next(p, w));
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -681,8 +805,6 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
 }  // namespace
 
 int tile_blocks() { return std::min(1024, num_sms()); }
-
-size_t tile_workspace(int d) { return (size_t)tile_blocks() * (2 * part_floats(ITEM, d) * 4 + 2 * sizeof(int4)); }
 
 hcl_status_t launch_tiles(const Params& p, cudaStream_t st) {
   if (p.a.kv.d == 128) return p.a.kv.v ? launch_t<128, false>(p, st) : launch_t<128, true>(p, st);
