@@ -12,11 +12,11 @@
 // Numerics.  Codes are exact in fp16 and so is a query row after its exponent is taken out
 // (2^e with the row's largest magnitude in [2^14, 2^15)), so the fp16 products of Q K^T are
 // exact and summed in fp32:  z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
-// A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + 7) with
-// lv = log2(v_scale) and M >= max(z2 + lv) - 8 a running reference, rounded to fp16 (11 bits,
-// 39 binades below the largest), and O = sum P * code in fp32 needs no further scale.  The
+// A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + 4) with
+// lv = log2(v_scale) and M >= max(z2 + lv) - 11 a running reference, rounded to fp16 (11 bits
+// down to 2^-18 of the largest, nothing below 2^-29), and O = sum P * code in fp32 needs no further scale.  The
 // softmax sum has its own reference m = max z2 (l = sum 2^(z2 - m)), formed from the unrounded P
-// of each group of 16 rows (never more than one page) times 2^(M - 7 - lv - m).  lv is not taken
+// of each group of 16 rows (never more than one page) times 2^(M - 4 - lv - m).  lv is not taken
 // below the largest lv met so far minus 60 (a page of zeros has the scale 2^-126), which keeps
 // every factor in range; its values then count as less than 2^-60 of the largest page's.
 #pragma once
@@ -31,8 +31,8 @@ namespace paged {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float P_OFF = 7.f;       // P's largest magnitude is 2^P_OFF .. 2^(P_OFF + P_LAZY) <= 2^15
-constexpr float P_LAZY = 8.f;      // M may lag its maximum by this much
+constexpr float P_OFF = 4.f;       // P's largest magnitude is 2^P_OFF .. 2^(P_OFF + P_LAZY) <= 2^15
+constexpr float P_LAZY = 11.f;     // M may lag its maximum by this much
 constexpr float LV_SPAN = 60.f;
 constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126
 constexpr int ROWS_SMALL = 16;     // query rows (queries x heads of a KV head) of the row kernel

@@ -5,10 +5,13 @@
 // one request and KV head; a round is 128 KV rows.  Roles:
 //   warps 0-3 / 4-7   softmax of tile 0 / 1: one thread per query row; they also load Q and
 //                     write the output
-//   warps 8-11        widening: E4M3 codes from global memory (loaded a round ahead into
-//                     registers) to fp16 tiles in shared memory, 128-byte swizzle.  The same
-//                     layout serves K (K-major B operand of S = Q K^T) and V (MN-major B operand
-//                     of O += P V); rows that are both key and value are widened once.
+//   warp 14           loads: TMA boxes of E4M3 codes (a page, or 64 rows of a longer one) into
+//                     a ring of staging units of 64 rows, and the round's page parameters
+//   warps 8-11        widening: codes from the staging ring to fp16 tiles, 128-byte swizzle.
+//                     The same layout serves K (K-major B operand of S = Q K^T) and V (MN-major
+//                     B operand of O += P V); rows that are both key and value are widened once.
+//                     (Loading the codes straight into the widening threads' registers spent
+//                     more issue slots on addresses than on the conversion.)
 //   warp 13           one thread walks the block's items and describes them, up to four ahead
 //   warp 12           one thread issues every MMA:  PV_0(r), S_0(r+1), PV_1(r), S_1(r+1), so one
 //                     tile's softmax runs under the other tile's MMAs
@@ -30,13 +33,14 @@ namespace {
 
 constexpr int TILE = 128;      // KV rows per round, query rows per tile
 constexpr int ITEM = ROWS_ITEM;  // query rows per item
-constexpr int THREADS = 16 * 32;  // warps 14, 15 idle (registers are handed out by fours of warps)
+constexpr int THREADS = 16 * 32;  // warp 15 idle (registers are handed out by fours of warps)
 constexpr int PRING = 8;       // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
 struct RoundPar {              // what the softmax needs of a round's pages (groups of 16 rows)
   float kc[8], lv[8], wl[8];   // scale2 * k_scale, log2(v_scale), 2^(lvref - lv)
-  uint32_t valid[4], poison[4];
+  uint32_t valid[4];           // rows whose page is in the cache
+  uint32_t poison[4];          // edge rounds: rows with a NaN value, by widening warp (see look())
   float lvref;
   uint32_t edge;               // some query row of the item does not see the round whole
   float pad[6];
@@ -143,24 +147,28 @@ template <int D, bool SHARED>
 struct Cfg {
   static constexpr int PIECES = D / 16;               // 16-code pieces of a row
   static constexpr int RPP = 128 / PIECES;            // rows per pass of the widening threads
-  static constexpr int PASSES = TILE / RPP;
+  static constexpr int RPW = RPP / 4;                 // of which each of their warps has RPW
+  static constexpr int UNIT = 64;                     // rows of a staging unit
+  static constexpr int NU = 3;                        // staging units
   static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile, and of a K or V tile
   static constexpr int NK = SHARED ? 4 : 2;           // K (or shared) tiles in the ring
   static constexpr int NV = SHARED ? 4 : 2;
   static constexpr uint32_t K = 2 * QT;
   static constexpr uint32_t V = SHARED ? K : K + NK * QT;
-  static constexpr uint32_t PAR = K + 4 * QT;
+  static constexpr uint32_t STAGE = K + 4 * QT;
+  static constexpr uint32_t PAR = STAGE + NU * UNIT * D;
   static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
   static constexpr uint32_t ITEMS = STAT + 128 * 16;
   static constexpr uint32_t BAR = ITEMS + IRING * sizeof(Item);
-  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 2 + 2 + 1 + 2 * IRING;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 2 + 2 + 1 + 2 * IRING + 2 * NU;
   static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
   static constexpr uint32_t MISC = SCRATCH + (16 + 4) * 8;
   static constexpr uint32_t TOTAL = MISC + 16;
 };
 
 template <int D, bool SHARED>
-__global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_tile_kernel(const Params p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   using C = Cfg<D, SHARED>;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset: the compiler still sees shared memory)
@@ -177,6 +185,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
   uint64_t* drain = s_full + 8;
   uint64_t* i_full = s_full + 9;             // [IRING] an item's description stands
   uint64_t* i_empty = i_full + IRING;        // [IRING] every role is done with it
+  uint64_t* u_full = i_empty + IRING;        // [NU] a staging unit's codes landed, its round's parameters stand
+  uint64_t* u_empty = u_full + C::NU;        // [NU] the widening warps have read it
   Item* items = reinterpret_cast<Item*>(sm + C::ITEMS);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + C::MISC + 4);
@@ -190,9 +200,12 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       mbar_init(&q_full[t], 128);
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < IRING; i++) { mbar_init(&i_full[i], 1); mbar_init(&i_empty[i], 128 + 256 + 1); }
+    for (int i = 0; i < IRING; i++) { mbar_init(&i_full[i], 1); mbar_init(&i_empty[i], 4 + 8 + 1 + 1); }
+    for (int i = 0; i < C::NU; i++) { mbar_init(&u_full[i], 1); mbar_init(&u_empty[i], 4); }
     *s_abort = 0;
     fence_barrier_init();
+    prefetch_tmap(&tk);
+    if (!SHARED) prefetch_tmap(&tv);
   }
   if (warp == 12) {
     tmem_alloc(s_tmem, 512);
@@ -245,158 +258,92 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
   const bool any = share.u1 > share.u0;
   if (!any && tid == 0) p.meta[blockIdx.x].ends = 0;
 
-  // registers of the four warpgroups: 152 + 152 + 120 + 88 = 4 * 128
+  // registers of the four warpgroups: 176 + 176 + 64 + 96 = 4 * 128
   if (any && warp >= 8 && warp < 12) {
     // ------------------------------------------------------------------ widening
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    const int wt = tid - 256, pc = wt % C::PIECES, pr = wt / C::PIECES;
-    const uint8_t* kcodes = static_cast<const uint8_t*>(p.a.kv.k);
-    const uint8_t* vcodes = static_cast<const uint8_t*>(p.a.kv.v);
-    const int pmask = p.a.kv.page - 1;
-    bool ok = true, fault = false;
-    uint32_t rg = 0;  // rounds so far
-    for (uint32_t it = 0;; it++) {
-      const Item* im = items + it % IRING;
-      ok = mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
-      ok = !bar_or(2, 128, !ok);
-      const int count = ok ? im->count : 0;
-      if (count == 0) break;
-      const int all_lo = im->all_lo, all_hi = im->all_hi, any_hi = im->any_hi, jfirst = im->j0, g = im->g;
-      const int32_t* trow = p.a.table + (size_t)im->b * p.a.max_pages;
-      // page of KV row j: -2 where no row is wanted, -1 for an id outside the cache
-      auto page_at = [&](int j) {
-        int id = j < any_hi ? __ldg(trow + (j >> p.sh)) : -2;
-        if (id != -2 && (id < 0 || id >= p.a.kv.n_pages)) { id = -1; fault = true; }
-        return id;
-      };
-      auto load_ids = [&](int i, int (&id)[C::PASSES]) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int ww = warp - 8, pc = lane % C::PIECES, pr = lane / C::PIECES;
+    // this thread's place in a pass of a staging unit and of a tile; the two 64-dimension halves
+    // take a piece's two 16-byte parts in opposite order: no bank conflict
+    const int row0 = ww * C::RPW + pr;
+    const uint32_t src0 = C::STAGE + row0 * D + pc * 16;
+    const int c0 = (pc & 3) * 2, sw = row0 & 7;  // (RPP is a multiple of 8: every pass has the same row & 7)
+    const uint32_t dst0 = (pc >> 2) * 16384 + row0 * 128;
+    const uint32_t first = dst0 + (((pc & 4 ? c0 + 1 : c0) ^ sw) << 4), second = dst0 + (((pc & 4 ? c0 : c0 + 1) ^ sw) << 4);
+    bool ok = true;
+    uint32_t rg = 0, u = 0;  // rounds, staging units so far
+    // one tile: two staging units into `tile`
+    auto widen = [&](uint8_t* tile, RoundPar* rp, bool mark) {
+      uint32_t bad = 0;
+      bool edge = false;
 #pragma unroll
-        for (int q = 0; q < C::PASSES; q++) id[q] = i < count ? page_at(jfirst + i * TILE + q * C::RPP + pr) : -2;
-      };
-      auto load_codes = [&](const uint8_t* codes, int i, const int (&id)[C::PASSES], uint4 (&x)[C::PASSES]) {
+      for (int h = 0; h < 2; h++, u++) {
+        const uint32_t su = u % C::NU;
+        ok = ok && mbar_wait(&u_full[su], (u / C::NU) & 1, p.limit, s_abort);
+        edge = rp->edge;
+        uint4 x[C::UNIT / C::RPP];
 #pragma unroll
-        for (int q = 0; q < C::PASSES; q++) {
-          const int j = jfirst + i * TILE + q * C::RPP + pr;
-          x[q] = make_uint4(0, 0, 0, 0);
-          if (id[q] >= 0 && j < any_hi)
-            x[q] = __ldg(reinterpret_cast<const uint4*>(
-                codes + ((((size_t)id[q] * p.a.kv.Hkv + g) << p.sh) + (j & pmask)) * D + pc * 16));
+        for (int q = 0; q < C::UNIT / C::RPP; q++)
+          x[q] = *reinterpret_cast<const uint4*>(sm + src0 + su * (C::UNIT * D) + q * C::RPP * D);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&u_empty[su]);
+        if (edge && mark) {
+          // Not every query row sees the whole round: NaN codes become 0 (0 * NaN would reach rows
+          // that do not see them; rows behind the last hold anything) and are noted for the softmax
+#pragma unroll
+          for (int q = 0; q < C::UNIT / C::RPP; q++) {
+            const uint4 n4 = make_uint4(nan_bytes(x[q].x), nan_bytes(x[q].y), nan_bytes(x[q].z), nan_bytes(x[q].w));
+            const bool n = (n4.x | n4.y | n4.z | n4.w) != 0;
+            if (n) x[q] = make_uint4(x[q].x & ~n4.x, x[q].y & ~n4.y, x[q].z & ~n4.z, x[q].w & ~n4.w);
+            const uint32_t who = __ballot_sync(~0u, n);
+#pragma unroll
+            for (int r = 0; r < C::RPW; r++)
+              if ((who >> (r * C::PIECES)) & ((1u << C::PIECES) - 1u))
+                bad |= 1u << ((h * (C::UNIT / C::RPP) + q) * C::RPW + r);
+          }
         }
-      };
-      auto store_tile = [&](uint8_t* tile, const uint4 (&x)[C::PASSES]) {
 #pragma unroll
-        for (int q = 0; q < C::PASSES; q++) {
-          const int row = q * C::RPP + pr;
+        for (int q = 0; q < C::UNIT / C::RPP; q++) {
           const uint4 lo = make_uint4(half2_of_codes(uint16_t(x[q].x)), half2_of_codes(uint16_t(x[q].x >> 16)),
                                       half2_of_codes(uint16_t(x[q].y)), half2_of_codes(uint16_t(x[q].y >> 16)));
           const uint4 hi = make_uint4(half2_of_codes(uint16_t(x[q].z)), half2_of_codes(uint16_t(x[q].z >> 16)),
                                       half2_of_codes(uint16_t(x[q].w)), half2_of_codes(uint16_t(x[q].w >> 16)));
-          uint8_t* base = tile + (pc >> 2) * 16384 + row * 128;
-          const int c0 = (pc & 3) * 2;
-          uint4* a0 = reinterpret_cast<uint4*>(base + ((c0 ^ (row & 7)) << 4));
-          uint4* a1 = reinterpret_cast<uint4*>(base + (((c0 + 1) ^ (row & 7)) << 4));
-          // the two 64-dimension halves start with different pieces: no bank conflict
-          if (pc & 4) { *a1 = hi; *a0 = lo; }
-          else { *a0 = lo; *a1 = hi; }
-        }
-      };
-      // NaN codes of a round that not all query rows see whole: the value becomes 0 (0 * NaN
-      // would reach rows that do not see it), and the softmax marks the rows that do see it
-      auto clean = [&](uint4 (&x)[C::PASSES], RoundPar* rp) {
-#pragma unroll
-        for (int q = 0; q < C::PASSES; q++) {
-          const uint4 n4 = make_uint4(nan_bytes(x[q].x), nan_bytes(x[q].y), nan_bytes(x[q].z), nan_bytes(x[q].w));
-          if (n4.x | n4.y | n4.z | n4.w) {
-            x[q] = make_uint4(x[q].x & ~n4.x, x[q].y & ~n4.y, x[q].z & ~n4.z, x[q].w & ~n4.w);
-            const int row = q * C::RPP + pr;
-            atomicOr(&rp->poison[row >> 5], 1u << (row & 31));
-          }
-        }
-      };
-      int id[C::PASSES];
-      uint4 kx[C::PASSES], vx[SHARED ? 1 : C::PASSES];
-      load_ids(0, id);
-      load_codes(kcodes, 0, id, kx);
-      if constexpr (!SHARED) load_codes(vcodes, 0, id, vx);
-      load_ids(1, id);
-      // page parameters: lane g8 of the first widening warp has group g8
-      int gid = -2, gid_next = -2;
-      float gks = 0.f, gvs = 0.f, lvref = -INFINITY;
-      auto group_page = [&](int i) { return i < count ? page_at(jfirst + i * TILE + (lane & 7) * 16) : -2; };
-      auto load_scales = [&](int i) {
-        gid = gid_next;
-        gid_next = group_page(i + 1);
-        if (gid >= 0) {
-          const size_t pg = (size_t)gid * p.a.kv.Hkv + g;
-          gks = __ldg(p.a.kv.k_scale + pg);
-          gvs = SHARED ? gks : __ldg(p.a.kv.v_scale + pg);
-        }
-      };
-      if (warp == 8) {
-        gid_next = group_page(0);
-        load_scales(0);
-      }
-      for (int i = 0; i < count; i++, rg++) {
-        const int kb = rg % C::NK;
-        RoundPar* rp = par + rg % PRING;
-        const int j0 = jfirst + i * TILE;
-        const bool edge = j0 < all_lo || j0 + TILE > all_hi;
-        uint64_t* ke = SHARED ? v_empty : k_empty;
-        if (rg >= C::NK) ok = ok && mbar_wait(&ke[kb], ((rg / C::NK) & 1) ^ 1, p.limit, s_abort);
-        if (warp == 8) {
-          const bool good = gid >= 0;
-          float lv = good ? log2_scale(gvs) : -INFINITY, mx = lv;
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-          lvref = fmaxf(lvref, mx);
-          const uint32_t gm = __ballot_sync(~0u, good) & 0xFF;
-          if (lane < 8) {
-            lv = fmaxf(lv, lvref - LV_SPAN);
-            rp->kc[lane] = good ? fmaxf(gks, SCALE_MIN) * p.scale2 : 0.f;
-            rp->lv[lane] = good ? lv : 0.f;
-            rp->wl[lane] = good ? ex2_ftz(lvref - lv) : 0.f;
-            if (lane < 4) {
-              rp->valid[lane] = ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
-              rp->poison[lane] = 0u;
-            }
-            if (lane == 0) {
-              rp->lvref = lvref == -INFINITY ? 0.f : lvref;
-              rp->edge = edge;
-            }
-          }
-        }
-        // the parameters stand before any thread marks a poisoned row
-        if (bar_or(2, 128, !ok)) { ok = false; break; }
-        if (SHARED && edge) clean(kx, rp);
-        store_tile(sm + C::K + kb * C::QT, kx);
-        fence_proxy_async_smem();
-        mbar_arrive(&k_full[kb]);
-        load_codes(kcodes, i + 1, id, kx);
-        if (warp == 8) load_scales(i + 1);
-        if constexpr (SHARED) load_ids(i + 2, id);
-        if constexpr (!SHARED) {
-          const int vb = rg % C::NV;
-          if (rg >= C::NV) ok = ok && mbar_wait(&v_empty[vb], ((rg / C::NV) & 1) ^ 1, p.limit, s_abort);
-          if (edge) clean(vx, rp);
-          store_tile(sm + C::V + vb * C::QT, vx);
-          fence_proxy_async_smem();
-          mbar_arrive(&v_full[vb]);
-          load_codes(vcodes, i + 1, id, vx);
-          load_ids(i + 2, id);
+          const uint32_t off = (h * C::UNIT + q * C::RPP) * 128;
+          *reinterpret_cast<uint4*>(tile + first + off) = pc & 4 ? hi : lo;
+          *reinterpret_cast<uint4*>(tile + second + off) = pc & 4 ? lo : hi;
         }
       }
+      if (edge && mark && lane == 0) rp->poison[ww] = bad;
+      fence_proxy_async_smem();
+    };
+    for (uint32_t it = 0;; it++) {
+      ok = ok && mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
       ok = !bar_or(2, 128, !ok);  // the four warps go on, or end, together
-      mbar_arrive(&i_empty[it % IRING]);
-      if (!ok) break;
+      const int count = ok ? items[it % IRING].count : 0;
+      if (count == 0) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
+      for (int i = 0; i < count && ok; i++, rg++) {
+        RoundPar* rp = par + rg % PRING;
+        const uint32_t kb = rg % C::NK;
+        if (rg >= C::NK) ok = mbar_wait(&(SHARED ? v_empty : k_empty)[kb], ((rg / C::NK) & 1) ^ 1, p.limit, s_abort);
+        widen(sm + C::K + kb * C::QT, rp, SHARED);
+        mbar_arrive(&k_full[kb]);
+        if constexpr (!SHARED) {
+          const uint32_t vb = rg % C::NV;
+          if (rg >= C::NV) ok = ok && mbar_wait(&v_empty[vb], ((rg / C::NV) & 1) ^ 1, p.limit, s_abort);
+          widen(sm + C::V + vb * C::QT, rp, true);
+          mbar_arrive(&v_full[vb]);
+        }
+      }
     }
     if (!ok) {
       *s_abort = 1;
-      report(p.a.status, HCL_ERR_TIMEOUT);
+      if (lane == 0) report(p.a.status, HCL_ERR_TIMEOUT);
     }
-    if (fault) report(p.a.status, HCL_ERR_DEVICE_FAULT);
   } else if (any && warp >= 12) {
     // ------------------------------------------------------------------ MMA issuer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 12 && lane == 0) {
       const uint64_t dq = make_sdesc(smem_u32(sm), 16, 1024, SMEM_SWIZZLE_128B);
       const uint64_t dk = make_sdesc(smem_u32(sm + C::K), 16, 1024, SMEM_SWIZZLE_128B);
@@ -478,6 +425,90 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       umma_commit(drain);
       if (!mbar_wait(drain, 0, p.limit, nullptr)) report(p.a.status, HCL_ERR_TIMEOUT);
     }
+    if (warp == 14) {
+      // ---------------------------------------------------------------- loads
+      const int box = min(p.a.kv.page, C::UNIT), pmask = p.a.kv.page - 1, g8 = lane & 7;
+      const bool begins = lane < 8 && (g8 & (box / 16 - 1)) == 0;  // this lane's 16-row group begins a box
+      bool ok = true, fault = false;
+      uint32_t rg = 0, u = 0;
+      for (uint32_t it = 0; ok; it++) {
+        ok = __all_sync(~0u, mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort));
+        const Item im = items[it % IRING];
+        if (!ok || im.count == 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
+        const int32_t* trow = p.a.table + (size_t)im.b * p.a.max_pages;
+        // the page of this lane's group in round i: -2 where no row is wanted
+        auto page_at = [&](int i) {
+          const int j = im.j0 + i * TILE + g8 * 16;
+          return i < im.count && j < im.any_hi ? __ldg(trow + (j >> p.sh)) : -2;
+        };
+        auto good_page = [&](int id) { return (uint32_t)id < (uint32_t)p.a.kv.n_pages; };
+        auto scales = [&](int id, float* ks, float* vs) {
+          *ks = *vs = 1.f;
+          if (good_page(id)) {
+            const size_t pg = (size_t)id * p.a.kv.Hkv + im.g;
+            *ks = __ldg(p.a.kv.k_scale + pg);
+            *vs = SHARED ? *ks : __ldg(p.a.kv.v_scale + pg);
+          }
+        };
+        float lvref = -INFINITY, ks, vs, ks1, vs1;
+        int id = page_at(0), id1 = page_at(1);  // ids two rounds ahead, scales one
+        scales(id, &ks, &vs);
+        for (int i = 0; i < im.count && ok; i++, rg++) {
+          const int id2 = page_at(i + 2);
+          scales(id1, &ks1, &vs1);
+          const bool good = good_page(id);
+          fault |= !good && id != -2;
+          const int j0 = im.j0 + i * TILE;
+          float lv = good ? log2_scale(vs) : -INFINITY, mx = lv;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+          lvref = fmaxf(lvref, mx);
+          const uint32_t gm = __ballot_sync(~0u, good) & 0xFF;
+          const uint32_t boxes = __ballot_sync(~0u, good && begins);
+          const int row = (int)(((long long)id * p.a.kv.Hkv + im.g) << p.sh) + ((j0 + g8 * 16) & pmask);
+#pragma unroll
+          for (int h = 0; h < (SHARED ? 2 : 4); h++, u++) {
+            const uint32_t su = u % C::NU;
+            if (u >= C::NU) ok = ok && __all_sync(~0u, mbar_wait(&u_empty[su], ((u / C::NU) & 1) ^ 1, p.limit, s_abort));
+            if (!ok) break;
+            if (h == 0) {
+              RoundPar* rp = par + rg % PRING;
+              if (lane < 8) {
+                lv = fmaxf(lv, lvref - LV_SPAN);
+                rp->kc[lane] = good ? fmaxf(ks, SCALE_MIN) * p.scale2 : 0.f;
+                rp->lv[lane] = good ? lv : 0.f;
+                rp->wl[lane] = good ? ex2_ftz(lvref - lv) : 0.f;
+                if (lane < 4)
+                  rp->valid[lane] =
+                      ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
+                if (lane == 0) {
+                  rp->lvref = lvref == -INFINITY ? 0.f : lvref;
+                  rp->edge = j0 < im.all_lo || j0 + TILE > im.all_hi || gm != 0xFF;
+                }
+              }
+              __syncwarp();
+            }
+            const uint32_t half = 0xFu << (4 * (h & 1));
+            if (lane == 0) mbar_arrive_expect_tx(&u_full[su], __popc(boxes & half) * box * D);
+            __syncwarp();
+            if ((boxes & half) >> lane & 1)
+              tma_load_2d(sm + C::STAGE + su * (C::UNIT * D) + (g8 & 3) * 16 * D, h < 2 ? &tk : &tv, &u_full[su], 0, row);
+          }
+          id = id1; id1 = id2; ks = ks1; vs = vs1;
+        }
+      }
+      if (!ok) {
+        *s_abort = 1;
+        if (lane == 0) report(p.a.status, HCL_ERR_TIMEOUT);
+      }
+      if (fault) report(p.a.status, HCL_ERR_DEVICE_FAULT);
+      // every copy has landed before the block's shared memory goes away
+      for (uint32_t k = u > C::NU ? u - C::NU : 0; k < u; k++)
+        if (!mbar_wait(&u_full[k % C::NU], (k / C::NU) & 1, p.limit, nullptr) && lane == 0)
+          report(p.a.status, HCL_ERR_TIMEOUT);
+    }
     if (warp == 13 && lane == 0) {
       // ---------------------------------------------------------------- the items
       Walk w;
@@ -524,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
     __syncwarp();
   } else if (any && warp < 8) {
     // ------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lq = uint32_t((warp & 3) * 32) << 16;
     const uint32_t tS = tbase + lq + t * TILE, tO = tbase + lq + O_COL + t * 128;
@@ -589,9 +620,13 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       auto look = [&](uint32_t R, int j0) {
         const RoundPar* rp = par + R % PRING;
         if (!rp->edge) return;
-#pragma unroll
+        // bit q * RPW + r of widening warp v's word: row q * RPP + v * RPW + r
+#pragma unroll 1
         for (int v = 0; v < 4; v++)
-          if (rp->poison[v] & range_mask(j0 + 32 * v, lo, hi)) sick = true;
+          for (uint32_t bits = rp->poison[v]; bits; bits &= bits - 1) {
+            const int e = __ffs(bits) - 1, r = (e / C::RPW) * C::RPP + v * C::RPW + e % C::RPW;
+            sick |= j0 + r >= lo && j0 + r < hi && ((rp->valid[r >> 5] >> (r & 31)) & 1u);
+          }
       };
       for (int k = 0; k < steps; k++) {
         const int rr = pair ? k : 2 * k + t;
@@ -643,14 +678,16 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
         // O is stable: S of this step was issued behind the completed PV of the last one
         if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll
-          for (int q = 0; q < D / 16; q++) {
-            uint32_t r16[16];
-            tmem_ld16(tO + q * 16, r16);
+          for (int c = 0; c < D / 64; c++) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) tmem_ld16(tO + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; j++) r16[j] = __float_as_uint(__uint_as_float(r16[j]) * al);
-            tmem_st16(tO + q * 16, r16);
+            for (int j = 0; j < 64; j++) sv[j] = __float_as_uint(__uint_as_float(sv[j]) * al);
+#pragma unroll
+            for (int q = 0; q < 4; q++) tmem_st16(tO + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
           }
+          load_scores(0);
         }
         const float Mu = M == -INFINITY ? 0.f : M, mu = m == -INFINITY ? 0.f : m;
         // P over the first half of S: columns 64 c .. + 63 go to columns 32 c .. + 31, whose scores
@@ -778,7 +815,8 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
       // O is read and the exchange buffer is free before the next item's Q
       tc_fence_before();
       if (!pair) asm volatile("bar.sync 4, 256;" ::: "memory");
-      mbar_arrive(&i_empty[it % IRING]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
       rg += n;
       step += steps;
     }
@@ -793,12 +831,21 @@ __global__ void __launch_bounds__(THREADS, 1) paged_tile_kernel(const Params p) 
 
 template <int D, bool SHARED>
 hcl_status_t launch_t(const Params& p, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  const int box = std::min(p.a.kv.page, 64);
+  hcl_status_t e = code_map(&tk, p.a.kv.k, p.a.kv, box, false);
+  if (e != HCL_OK) return e;
+  tv = tk;
+  if (!SHARED) {
+    e = code_map(&tv, p.a.kv.v, p.a.kv, box, false);
+    if (e != HCL_OK) return e;
+  }
   auto kern = paged_tile_kernel<D, SHARED>;
   const int smem = (int)Cfg<D, SHARED>::TOTAL + 1024;
   static_assert(Cfg<D, SHARED>::TOTAL + 1024 <= 232448, "shared memory");
-  hcl_status_t e = set_kernel_attrs(reinterpret_cast<const void*>(kern), smem, false);
+  e = set_kernel_attrs(reinterpret_cast<const void*>(kern), smem, false);
   if (e != HCL_OK) return e;
-  return check_cuda(launch_pdl(kern, dim3(p.n_blocks), dim3(THREADS), (size_t)smem, st, 1, p),
+  return check_cuda(launch_pdl(kern, dim3(p.n_blocks), dim3(THREADS), (size_t)smem, st, 1, p, tk, tv),
                     "paged attention (tiles) launch");
 }
 
