@@ -2,9 +2,17 @@
 // head > 16): prompts, chunks, and decode with many heads on one KV head.  tcgen05 tensor cores.
 //
 // One persistent block per SM.  An item is 256 query rows (two tiles of 128, the M of an MMA) of
-// one request and KV head; a round is 128 KV rows.  Roles:
+// one request and KV head; a round is 64 KV rows.  Roles:
 //   warps 0-3 / 4-7   softmax of tile 0 / 1: one thread per query row; they also load Q and
 //                     write the output
+//   warps 12, 15      issue the MMAs of tile 0, 1.  (The tensor pipe takes hardly more than the
+//                     MMA it works on, so what one issuer spends on its barriers must pass under
+//                     the other's MMAs.)  Each tile has two score buffers: S(r+1) is
+//                     issued before PV(r), so a softmax group finds its next scores ready and
+//                     waits for MMAs only where O has to be rescaled.  (With one buffer and
+//                     rounds of 128, the chain softmax -> PV -> S -> softmax took 6100 clocks a
+//                     round of which the tensor cores worked 2050.)
+//   warp 13           one thread walks the block's items and describes them, up to four ahead
 //   warp 14           loads: TMA boxes of E4M3 codes (a page, or 64 rows of a longer one) into
 //                     a ring of staging units of 64 rows, and the round's page parameters
 //   warps 8-11        widening: codes from the staging ring to fp16 tiles, 128-byte swizzle.
@@ -12,17 +20,14 @@
 //                     B operand of O += P V); rows that are both key and value are widened once.
 //                     (Loading the codes straight into the widening threads' registers spent
 //                     more issue slots on addresses than on the conversion.)
-//   warp 13           one thread walks the block's items and describes them, up to four ahead
-//   warp 12           one thread issues every MMA:  PV_0(r), S_0(r+1), PV_1(r), S_1(r+1), so one
-//                     tile's softmax runs under the other tile's MMAs
 // P (fp16) is written over the first half of its S in tensor memory and read there as the A
-// operand.  TMEM: S_0 / P_0, S_1 / P_1, O_0, O_1.
+// operand.  TMEM: S_0 / P_0 and S_1 / P_1 (two buffers of 64 columns each), O_0, O_1.
 // An item of at most 128 rows (decode over many heads, a request's last rows) runs in single
 // mode: both softmax groups work on the same rows, group t on the rounds of parity t with its
 // own O, and join at the end, so the pipeline keeps its two streams.
 //
-// Bound by the MMA rate and, equally, the exponentials (256 x 128 a round at 16 a clock take as
-// long as the round's MMAs); decode over many heads by the widening and softmax of each round.
+// Bound by the MMA rate and, equally, the exponentials (256 x 64 a round at 16 a clock take as
+// long as the round's MMAs); decode over many heads by the latency of each round's softmax.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -31,32 +36,55 @@ namespace hcl {
 namespace paged {
 namespace {
 
-constexpr int TILE = 128;      // KV rows per round, query rows per tile
+constexpr int TILE = 64;       // KV rows per round
 constexpr int ITEM = ROWS_ITEM;  // query rows per item
-constexpr int THREADS = 16 * 32;  // warp 15 idle (registers are handed out by fours of warps)
-constexpr int PRING = 8;       // rounds whose page parameters are kept
+constexpr int THREADS = 16 * 32;
+constexpr int PRING = 16;      // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
 struct RoundPar {              // what the softmax needs of a round's pages (groups of 16 rows)
-  float kc[8], lv[8], wl[8];   // scale2 * k_scale, log2(v_scale), 2^(lvref - lv)
-  uint32_t valid[4];           // rows whose page is in the cache
+  float kc[4], lv[4], wl[4];   // scale2 * k_scale, log2(v_scale), 2^(lvref - lv)
   uint32_t poison[4];          // edge rounds: rows with a NaN value, by widening warp (see look())
+  uint32_t valid[2];           // rows whose page is in the cache
   float lvref;
   uint32_t edge;               // some query row of the item does not see the round whole
-  float pad[6];
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
-// D (+)= A B with A (packed fp16 pairs) read from tensor memory.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The MMA warp runs as one: all lanes take the same path (so that descriptors and addresses stay
+// in uniform registers) and `lead`, true in one lane, predicates each instruction.  Issued from
+// inside a one-lane branch the same MMAs took 75 to 108 clocks each, with 48 to 64 of work.
+// Descriptors are given by their low words; the high words (swizzle, stride) are constants.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (SMEM_SWIZZLE_128B << 29);
+// D (+)= A B, both from shared memory.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(lead), "n"(DESC_HI)
+      : "memory");
+}
+// D (+)= A B with A (packed fp16 pairs) read from tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(lead), "n"(DESC_HI)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 // Barrier `id` over n threads; returns whether any of them passed true.
@@ -148,19 +176,20 @@ struct Cfg {
   static constexpr int PIECES = D / 16;               // 16-code pieces of a row
   static constexpr int RPP = 128 / PIECES;            // rows per pass of the widening threads
   static constexpr int RPW = RPP / 4;                 // of which each of their warps has RPW
-  static constexpr int UNIT = 64;                     // rows of a staging unit
-  static constexpr int NU = 3;                        // staging units
-  static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile, and of a K or V tile
-  static constexpr int NK = SHARED ? 4 : 2;           // K (or shared) tiles in the ring
-  static constexpr int NV = SHARED ? 4 : 2;
+  static constexpr int NU = 3;                        // staging units (a plane of a round each)
+  static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile
+  static constexpr uint32_t KT = TILE * D * 2;        // bytes of a K or V tile
+  static constexpr uint32_t HALF = TILE * 128;        // its two halves of 64 dimensions
+  static constexpr int NK = SHARED ? 8 : 4;           // K (or shared) tiles in the ring
+  static constexpr int NV = NK;
   static constexpr uint32_t K = 2 * QT;
-  static constexpr uint32_t V = SHARED ? K : K + NK * QT;
-  static constexpr uint32_t STAGE = K + 4 * QT;
-  static constexpr uint32_t PAR = STAGE + NU * UNIT * D;
+  static constexpr uint32_t V = SHARED ? K : K + NK * KT;
+  static constexpr uint32_t STAGE = K + 8 * KT;
+  static constexpr uint32_t PAR = STAGE + NU * TILE * D;
   static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
   static constexpr uint32_t ITEMS = STAT + 128 * 16;
   static constexpr uint32_t BAR = ITEMS + IRING * sizeof(Item);
-  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 2 + 2 + 1 + 2 * IRING + 2 * NU;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 4 + 4 + 2 + 2 + 1 + 2 * IRING + 2 * NU;
   static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
   static constexpr uint32_t MISC = SCRATCH + (16 + 4) * 8;
   static constexpr uint32_t TOTAL = MISC + 16;
@@ -178,12 +207,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* k_empty = k_full + C::NK;
   uint64_t* v_full = k_empty + C::NK;
   uint64_t* v_empty = v_full + C::NV;
-  uint64_t* s_full = v_empty + C::NV;  // [2] S of the step in TMEM
-  uint64_t* p_full = s_full + 2;       // [2] P in TMEM, O rescaled
-  uint64_t* o_done = s_full + 4;       // [2] PV of the step completed
-  uint64_t* q_full = s_full + 6;       // [2] Q tile in shared memory
-  uint64_t* drain = s_full + 8;
-  uint64_t* i_full = s_full + 9;             // [IRING] an item's description stands
+  uint64_t* s_full = v_empty + C::NV;        // [tile][buffer] S of a step in TMEM
+  uint64_t* p_full = s_full + 4;             // [tile][buffer] P in TMEM, O rescaled
+  uint64_t* o_done = s_full + 8;             // [tile] PV of the step completed
+  uint64_t* q_full = s_full + 10;            // [tile] Q tile in shared memory
+  uint64_t* drain = s_full + 12;
+  uint64_t* i_full = s_full + 13;            // [IRING] an item's description stands
   uint64_t* i_empty = i_full + IRING;        // [IRING] every role is done with it
   uint64_t* u_full = i_empty + IRING;        // [NU] a staging unit's codes landed, its round's parameters stand
   uint64_t* u_empty = u_full + C::NU;        // [NU] the widening warps have read it
@@ -191,16 +220,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + C::MISC + 4);
   if (tid == 0) {
-    for (int i = 0; i < C::NK; i++) { mbar_init(&k_full[i], 128); mbar_init(&k_empty[i], 1); }
-    for (int i = 0; i < C::NV; i++) { mbar_init(&v_full[i], 128); mbar_init(&v_empty[i], 1); }
+    for (int i = 0; i < C::NK; i++) { mbar_init(&k_full[i], 128); mbar_init(&k_empty[i], 2); }
+    for (int i = 0; i < C::NV; i++) { mbar_init(&v_full[i], 128); mbar_init(&v_empty[i], 2); }
+    for (int i = 0; i < 4; i++) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 128); }
     for (int t = 0; t < 2; t++) {
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 128);
       mbar_init(&o_done[t], 1);
       mbar_init(&q_full[t], 128);
     }
-    mbar_init(drain, 1);
-    for (int i = 0; i < IRING; i++) { mbar_init(&i_full[i], 1); mbar_init(&i_empty[i], 4 + 8 + 1 + 1); }
+    mbar_init(drain, 2);
+    for (int i = 0; i < IRING; i++) { mbar_init(&i_full[i], 1); mbar_init(&i_empty[i], 4 + 8 + 2 + 1); }
     for (int i = 0; i < C::NU; i++) { mbar_init(&u_full[i], 1); mbar_init(&u_empty[i], 4); }
     *s_abort = 0;
     fence_barrier_init();
@@ -268,52 +296,48 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int row0 = ww * C::RPW + pr;
     const uint32_t src0 = C::STAGE + row0 * D + pc * 16;
     const int c0 = (pc & 3) * 2, sw = row0 & 7;  // (RPP is a multiple of 8: every pass has the same row & 7)
-    const uint32_t dst0 = (pc >> 2) * 16384 + row0 * 128;
+    const uint32_t dst0 = (pc >> 2) * C::HALF + row0 * 128;
     const uint32_t first = dst0 + (((pc & 4 ? c0 + 1 : c0) ^ sw) << 4), second = dst0 + (((pc & 4 ? c0 : c0 + 1) ^ sw) << 4);
     bool ok = true;
     uint32_t rg = 0, u = 0;  // rounds, staging units so far
-    // one tile: two staging units into `tile`
+    // one staging unit into `tile`
     auto widen = [&](uint8_t* tile, RoundPar* rp, bool mark) {
-      uint32_t bad = 0;
-      bool edge = false;
+      constexpr int NQ = TILE / C::RPP;
+      const uint32_t su = u % C::NU;
+      ok = ok && mbar_wait(&u_full[su], (u / C::NU) & 1, p.limit, s_abort);
+      const bool edge = rp->edge && mark;
+      uint4 x[NQ];
 #pragma unroll
-      for (int h = 0; h < 2; h++, u++) {
-        const uint32_t su = u % C::NU;
-        ok = ok && mbar_wait(&u_full[su], (u / C::NU) & 1, p.limit, s_abort);
-        edge = rp->edge;
-        uint4 x[C::UNIT / C::RPP];
+      for (int q = 0; q < NQ; q++)
+        x[q] = *reinterpret_cast<const uint4*>(sm + src0 + su * (TILE * D) + q * C::RPP * D);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_empty[su]);
+      u++;
+      if (edge) {
+        // Not every query row sees the whole round: NaN codes become 0 (0 * NaN would reach rows
+        // that do not see them; rows behind the last hold anything) and are noted for the softmax
+        uint32_t bad = 0;
 #pragma unroll
-        for (int q = 0; q < C::UNIT / C::RPP; q++)
-          x[q] = *reinterpret_cast<const uint4*>(sm + src0 + su * (C::UNIT * D) + q * C::RPP * D);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&u_empty[su]);
-        if (edge && mark) {
-          // Not every query row sees the whole round: NaN codes become 0 (0 * NaN would reach rows
-          // that do not see them; rows behind the last hold anything) and are noted for the softmax
+        for (int q = 0; q < NQ; q++) {
+          const uint4 n4 = make_uint4(nan_bytes(x[q].x), nan_bytes(x[q].y), nan_bytes(x[q].z), nan_bytes(x[q].w));
+          const bool n = (n4.x | n4.y | n4.z | n4.w) != 0;
+          if (n) x[q] = make_uint4(x[q].x & ~n4.x, x[q].y & ~n4.y, x[q].z & ~n4.z, x[q].w & ~n4.w);
+          const uint32_t who = __ballot_sync(~0u, n);
 #pragma unroll
-          for (int q = 0; q < C::UNIT / C::RPP; q++) {
-            const uint4 n4 = make_uint4(nan_bytes(x[q].x), nan_bytes(x[q].y), nan_bytes(x[q].z), nan_bytes(x[q].w));
-            const bool n = (n4.x | n4.y | n4.z | n4.w) != 0;
-            if (n) x[q] = make_uint4(x[q].x & ~n4.x, x[q].y & ~n4.y, x[q].z & ~n4.z, x[q].w & ~n4.w);
-            const uint32_t who = __ballot_sync(~0u, n);
-#pragma unroll
-            for (int r = 0; r < C::RPW; r++)
-              if ((who >> (r * C::PIECES)) & ((1u << C::PIECES) - 1u))
-                bad |= 1u << ((h * (C::UNIT / C::RPP) + q) * C::RPW + r);
-          }
+          for (int r = 0; r < C::RPW; r++)
+            if ((who >> (r * C::PIECES)) & ((1u << C::PIECES) - 1u)) bad |= 1u << (q * C::RPW + r);
         }
-#pragma unroll
-        for (int q = 0; q < C::UNIT / C::RPP; q++) {
-          const uint4 lo = make_uint4(half2_of_codes(uint16_t(x[q].x)), half2_of_codes(uint16_t(x[q].x >> 16)),
-                                      half2_of_codes(uint16_t(x[q].y)), half2_of_codes(uint16_t(x[q].y >> 16)));
-          const uint4 hi = make_uint4(half2_of_codes(uint16_t(x[q].z)), half2_of_codes(uint16_t(x[q].z >> 16)),
-                                      half2_of_codes(uint16_t(x[q].w)), half2_of_codes(uint16_t(x[q].w >> 16)));
-          const uint32_t off = (h * C::UNIT + q * C::RPP) * 128;
-          *reinterpret_cast<uint4*>(tile + first + off) = pc & 4 ? hi : lo;
-          *reinterpret_cast<uint4*>(tile + second + off) = pc & 4 ? lo : hi;
-        }
+        if (lane == 0) rp->poison[ww] = bad;
       }
-      if (edge && mark && lane == 0) rp->poison[ww] = bad;
+#pragma unroll
+      for (int q = 0; q < NQ; q++) {
+        const uint4 lo = make_uint4(half2_of_codes(uint16_t(x[q].x)), half2_of_codes(uint16_t(x[q].x >> 16)),
+                                    half2_of_codes(uint16_t(x[q].y)), half2_of_codes(uint16_t(x[q].y >> 16)));
+        const uint4 hi = make_uint4(half2_of_codes(uint16_t(x[q].z)), half2_of_codes(uint16_t(x[q].z >> 16)),
+                                    half2_of_codes(uint16_t(x[q].w)), half2_of_codes(uint16_t(x[q].w >> 16)));
+        *reinterpret_cast<uint4*>(tile + first + q * C::RPP * 128) = pc & 4 ? hi : lo;
+        *reinterpret_cast<uint4*>(tile + second + q * C::RPP * 128) = pc & 4 ? lo : hi;
+      }
       fence_proxy_async_smem();
     };
     for (uint32_t it = 0;; it++) {
@@ -327,12 +351,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         RoundPar* rp = par + rg % PRING;
         const uint32_t kb = rg % C::NK;
         if (rg >= C::NK) ok = mbar_wait(&(SHARED ? v_empty : k_empty)[kb], ((rg / C::NK) & 1) ^ 1, p.limit, s_abort);
-        widen(sm + C::K + kb * C::QT, rp, SHARED);
+        widen(sm + C::K + kb * C::KT, rp, SHARED);
         mbar_arrive(&k_full[kb]);
         if constexpr (!SHARED) {
           const uint32_t vb = rg % C::NV;
           if (rg >= C::NV) ok = ok && mbar_wait(&v_empty[vb], ((rg / C::NV) & 1) ^ 1, p.limit, s_abort);
-          widen(sm + C::V + vb * C::QT, rp, true);
+          widen(sm + C::V + vb * C::KT, rp, true);
           mbar_arrive(&v_full[vb]);
         }
       }
@@ -344,91 +368,86 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (any && warp >= 12) {
     // ------------------------------------------------------------------ MMA issuer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    if (warp == 12 && lane == 0) {
-      const uint64_t dq = make_sdesc(smem_u32(sm), 16, 1024, SMEM_SWIZZLE_128B);
-      const uint64_t dk = make_sdesc(smem_u32(sm + C::K), 16, 1024, SMEM_SWIZZLE_128B);
-      const uint64_t dv = make_sdesc(smem_u32(sm + C::V), 16384, 1024, SMEM_SWIZZLE_128B);
+    if (warp == 12 || warp == 15) {
+      const int t = warp == 15;  // the tile
+      const uint32_t lead = lane == 0;
+      const uint32_t tb = __shfl_sync(~0u, tbase, 0) + t * 128;
+      const uint32_t sbase = smem_u32(sm);
+      const uint32_t dq = ((sbase & 0x3FFFFu) >> 4) | (1u << 16);
+      const uint32_t dk = (((sbase + C::K) & 0x3FFFFu) >> 4) | (1u << 16);
+      const uint32_t dv = (((sbase + C::V) & 0x3FFFFu) >> 4) | ((C::HALF >> 4) << 16);
       constexpr uint32_t idS = idesc_f16(128, TILE), idPV = idesc_f16(128, D) | (1u << 16);
-      // rg: rounds before this item; par_t: parity of tile t's step count; qp: of the items
-      uint32_t rg = 0, par0 = 0, par1 = 0, qp = 0;
+      // rg: rounds before this item; n: this tile's steps before this one; qp: parity of the items
+      uint32_t rg = 0, n = 0, qp = 0;
       bool ok = true;
-      // S of round R into tile t's scores, with the Q tile at aq
-      auto issue_s = [&](uint32_t R, int t, uint64_t aq, bool frees) {
+      auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity, p.limit, s_abort); };
+      // Both issuers release a K or V tile; where one of them alone uses it, it does so twice.
+      auto release = [&](uint64_t* bar, bool alone) {
+        commit_lead(bar, lead);
+        if (alone) commit_lead(bar, lead);
+      };
+      // scores of round R, this tile's step s, with the Q tile at aq
+      auto issue_s = [&](uint32_t R, uint32_t s, uint32_t aq, bool alone) {
         const uint32_t kb = R % C::NK;
-        ok = ok && mbar_wait(&k_full[kb], (R / C::NK) & 1, p.limit, s_abort);
+        wait(&k_full[kb], (R / C::NK) & 1);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t b0 = dk + uint64_t(kb * (C::QT >> 4));
+        const uint32_t b0 = dk + kb * (C::KT >> 4), d = tb + (s & 1) * TILE;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ks++) {
-          const uint32_t off = (ks >> 2) * (16384 >> 4) + (ks & 3) * 2;
-          umma_bf16(tbase + t * TILE, aq + off, b0 + off, idS, ks > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[t]);
-        if (!SHARED && frees) umma_commit(&k_empty[kb]);
+        for (int ks = 0; ks < D / 16; ks++)
+          umma_ss(d, aq + ((ks >> 2) * (16384 >> 4) + (ks & 3) * 2), b0 + ((ks >> 2) * (C::HALF >> 4) + (ks & 3) * 2), idS,
+                  ks > 0 ? 1u : 0u, lead);
+        commit_lead(&s_full[2 * t + (s & 1)], lead);
+        if (!SHARED) release(&k_empty[kb], alone);
       };
-      // O of tile t += P V of round R
-      auto issue_pv = [&](uint32_t R, int t, uint32_t parity, bool first, bool frees) {
-        const uint32_t vb = R % C::NV;
-        ok = ok && mbar_wait(&p_full[t], parity, p.limit, s_abort);
-        if (!SHARED) ok = ok && mbar_wait(&v_full[vb], (R / C::NV) & 1, p.limit, s_abort);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t b0 = dv + uint64_t(vb * (C::QT >> 4));
-#pragma unroll
-        for (int ks = 0; ks < 8; ks++)
-          umma_f16_ta(tbase + O_COL + t * 128, tbase + t * TILE + ks * 8, b0 + uint32_t(ks * (2048 >> 4)), idPV,
-                      ks > 0 || !first ? 1u : 0u);
-        umma_commit(&o_done[t]);
-        if (frees) umma_commit(&v_empty[vb]);
-      };
-      for (uint32_t it = 0; ok; it++) {
-        ok = mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
-        const int n = ok ? items[it % IRING].count : 0;
-        if (n == 0) break;
-        const bool pair = items[it % IRING].rows > 128;
-        mbar_arrive(&i_empty[it % IRING]);
-        ok = ok && mbar_wait(&q_full[0], qp, p.limit, s_abort);
-        if (pair) ok = ok && mbar_wait(&q_full[1], qp, p.limit, s_abort);
-        // tile t's step k is round k (pair) or 2k + t (single)
-        const uint64_t aq1 = pair ? dq + uint64_t(C::QT >> 4) : dq;
-        const int n0 = pair ? n : (n + 1) / 2, n1 = pair ? n : n / 2;
-        const uint32_t stride = pair ? 1 : 2, shift = pair ? 0 : 1;
-        issue_s(rg, 0, dq, !pair);
-        if (n1 > 0) issue_s(rg + shift, 1, aq1, true);
-        uint32_t R = rg;
-        for (int k = 0; k < n0 && ok; k++, R += stride) {
-          issue_pv(R, 0, par0, k == 0, !pair);
-          if (k + 1 < n0) {
-            // S_t of the next step overwrites P_t: PV_t must have completed
-            ok = ok && mbar_wait(&o_done[0], par0, p.limit, s_abort);
-            issue_s(R + stride, 0, dq, !pair);
-          }
-          par0 ^= 1;
-          if (k < n1) {
-            issue_pv(R + shift, 1, par1, k == 0, true);
-            if (k + 1 < n1) {
-              ok = ok && mbar_wait(&o_done[1], par1, p.limit, s_abort);
-              issue_s(R + stride + shift, 1, aq1, true);
-            }
-            par1 ^= 1;
-          }
-        }
-        rg += n;
+      for (uint32_t it = 0;; it++) {
+        wait(&i_full[it % IRING], (it / IRING) & 1);
+        ok = __all_sync(~0u, ok);
+        const int count = ok ? __shfl_sync(~0u, items[it % IRING].count, 0) : 0;
+        if (count == 0) break;
+        const bool pair = __shfl_sync(~0u, items[it % IRING].rows, 0) > 128;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
+        // this tile's step k is round k (pair) or 2k + t (single)
+        const int steps = pair ? count : (count + 1 - t) / 2;
+        const uint32_t aq = pair && t ? dq + (C::QT >> 4) : dq, stride = pair ? 1 : 2;
+        wait(&q_full[pair ? t : 0], qp);
         qp ^= 1;  // (group 1 arrives on q_full[1] in single mode too)
+        uint32_t R = rg + (pair ? 0 : t);
+        if (steps > 0) issue_s(R, n, aq, !pair);
+        for (int k = 0; k < steps && ok; k++, R += stride, n++) {
+          // the next step's scores go where P of the last step was: its PV must have completed
+          if (k + 1 < steps) {
+            if (k > 0) wait(&o_done[t], (n & 1) ^ 1);
+            issue_s(R + stride, n + 1, aq, !pair);
+          }
+          const uint32_t vb = R % C::NV;
+          if (!SHARED) wait(&v_full[vb], (R / C::NV) & 1);
+          wait(&p_full[2 * t + (n & 1)], (n >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t b0 = dv + vb * (C::KT >> 4), a0 = tb + (n & 1) * TILE;
+#pragma unroll
+          for (int ks = 0; ks < TILE / 16; ks++)
+            umma_ts(tb + O_COL, a0 + ks * 8, b0 + ks * (2048 >> 4), idPV, ks > 0 || k > 0 ? 1u : 0u, lead);
+          commit_lead(&o_done[t], lead);
+          release(&v_empty[vb], !pair);
+        }
+        rg += count;
       }
       if (!ok) {
         *s_abort = 1;
-        report(p.a.status, HCL_ERR_TIMEOUT);
+        if (lane == 0) report(p.a.status, HCL_ERR_TIMEOUT);
       }
       // every MMA issued has completed before TMEM may be freed
-      umma_commit(drain);
-      if (!mbar_wait(drain, 0, p.limit, nullptr)) report(p.a.status, HCL_ERR_TIMEOUT);
+      commit_lead(drain, lead);
+      if (!mbar_wait(drain, 0, p.limit, nullptr) && lane == 0) report(p.a.status, HCL_ERR_TIMEOUT);
+      __syncwarp();
     }
     if (warp == 14) {
       // ---------------------------------------------------------------- loads
-      const int box = min(p.a.kv.page, C::UNIT), pmask = p.a.kv.page - 1, g8 = lane & 7;
-      const bool begins = lane < 8 && (g8 & (box / 16 - 1)) == 0;  // this lane's 16-row group begins a box
+      const int box = min(p.a.kv.page, TILE), pmask = p.a.kv.page - 1, gr = lane & 3;
+      const bool begins = lane < 4 && (gr & (box / 16 - 1)) == 0;  // this lane's 16-row group begins a box
       bool ok = true, fault = false;
       uint32_t rg = 0, u = 0;
       for (uint32_t it = 0; ok; it++) {
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int32_t* trow = p.a.table + (size_t)im.b * p.a.max_pages;
         // the page of this lane's group in round i: -2 where no row is wanted
         auto page_at = [&](int i) {
-          const int j = im.j0 + i * TILE + g8 * 16;
+          const int j = im.j0 + i * TILE + gr * 16;
           return i < im.count && j < im.any_hi ? __ldg(trow + (j >> p.sh)) : -2;
         };
         auto good_page = [&](int id) { return (uint32_t)id < (uint32_t)p.a.kv.n_pages; };
@@ -463,38 +482,37 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int j0 = im.j0 + i * TILE;
           float lv = good ? log2_scale(vs) : -INFINITY, mx = lv;
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+          for (int o = 1; o < 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
           lvref = fmaxf(lvref, mx);
-          const uint32_t gm = __ballot_sync(~0u, good) & 0xFF;
+          const uint32_t gm = __ballot_sync(~0u, good) & 0xF;
           const uint32_t boxes = __ballot_sync(~0u, good && begins);
-          const int row = (int)(((long long)id * p.a.kv.Hkv + im.g) << p.sh) + ((j0 + g8 * 16) & pmask);
+          const int row = (int)(((long long)id * p.a.kv.Hkv + im.g) << p.sh) + ((j0 + gr * 16) & pmask);
 #pragma unroll
-          for (int h = 0; h < (SHARED ? 2 : 4); h++, u++) {
+          for (int h = 0; h < (SHARED ? 1 : 2); h++, u++) {
             const uint32_t su = u % C::NU;
             if (u >= C::NU) ok = ok && __all_sync(~0u, mbar_wait(&u_empty[su], ((u / C::NU) & 1) ^ 1, p.limit, s_abort));
             if (!ok) break;
             if (h == 0) {
               RoundPar* rp = par + rg % PRING;
-              if (lane < 8) {
+              if (lane < 4) {
                 lv = fmaxf(lv, lvref - LV_SPAN);
                 rp->kc[lane] = good ? fmaxf(ks, SCALE_MIN) * p.scale2 : 0.f;
                 rp->lv[lane] = good ? lv : 0.f;
                 rp->wl[lane] = good ? ex2_ftz(lvref - lv) : 0.f;
-                if (lane < 4)
+                if (lane < 2)
                   rp->valid[lane] =
                       ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
                 if (lane == 0) {
                   rp->lvref = lvref == -INFINITY ? 0.f : lvref;
-                  rp->edge = j0 < im.all_lo || j0 + TILE > im.all_hi || gm != 0xFF;
+                  rp->edge = j0 < im.all_lo || j0 + TILE > im.all_hi || gm != 0xF;
                 }
               }
               __syncwarp();
             }
-            const uint32_t half = 0xFu << (4 * (h & 1));
-            if (lane == 0) mbar_arrive_expect_tx(&u_full[su], __popc(boxes & half) * box * D);
+            if (lane == 0) mbar_arrive_expect_tx(&u_full[su], __popc(boxes) * box * D);
             __syncwarp();
-            if ((boxes & half) >> lane & 1)
-              tma_load_2d(sm + C::STAGE + su * (C::UNIT * D) + (g8 & 3) * 16 * D, h < 2 ? &tk : &tv, &u_full[su], 0, row);
+            if (boxes >> lane & 1)
+              tma_load_2d(sm + C::STAGE + su * (TILE * D) + gr * 16 * D, h == 0 ? &tk : &tv, &u_full[su], 0, row);
           }
           id = id1; id1 = id2; ks = ks1; vs = vs1;
         }
@@ -558,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int t = warp >> 2, row = tid & 127;
     const uint32_t lq = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tbase + lq + t * TILE, tO = tbase + lq + O_COL + t * 128;
+    const uint32_t tS = tbase + lq + t * 128, tO = tbase + lq + O_COL + t * 128;
     float* s_stat = reinterpret_cast<float*>(sm + C::STAT);
     uint32_t rg = 0, step = 0;
     bool ok = true;
@@ -628,46 +646,44 @@ __global__ void __launch_bounds__(THREADS, 1)
             sick |= j0 + r >= lo && j0 + r < hi && ((rp->valid[r >> 5] >> (r & 31)) & 1u);
           }
       };
+      const int back2 = pair ? 1 : 2;  // rounds from one step to the next
       for (int k = 0; k < steps; k++) {
         const int rr = pair ? k : 2 * k + t;
-        const uint32_t R = rg + rr;
+        const uint32_t R = rg + rr, n = step + k;
         const int j0 = jfirst + rr * TILE;
-        ok = mbar_wait(&s_full[t], (step + k) & 1, p.limit, s_abort);
+        const uint32_t tSn = tS + (n & 1) * TILE;
+        ok = mbar_wait(&s_full[2 * t + (n & 1)], (n >> 1) & 1, p.limit, s_abort);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        // (S of this step was issued behind PV of the last: that round's poison marks stand)
-        if (k > 0) look(R - (pair ? 1 : 2), j0 - (pair ? 1 : 2) * TILE);
+        // (these scores were issued behind PV of the step before the last: its marks stand)
+        if (k > 1) look(R - 2 * back2, j0 - 2 * back2 * TILE);
         const RoundPar* rp = par + R % PRING;
-        uint32_t vb[4];
+        uint32_t sv[TILE];
 #pragma unroll
-        for (int v = 0; v < 4; v++) vb[v] = range_mask(j0 + 32 * v, lo, hi) & rp->valid[v];
-        const bool clear = (vb[0] & vb[1] & vb[2] & vb[3]) == 0xFFFFFFFFu;
-        // scores of columns 64 c .. 64 c + 63, -inf where this row sees nothing
-        uint32_t sv[64];
-        auto load_scores = [&](int c) {
+        for (int q = 0; q < 4; q++) tmem_ld16(tSn + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
+        const float4 kc4 = *reinterpret_cast<const float4*>(rp->kc), lv4 = *reinterpret_cast<const float4*>(rp->lv);
+        const float4 wl4 = *reinterpret_cast<const float4*>(rp->wl);
+        const float lvref = rp->lvref;
+        const uint32_t vb[2] = {range_mask(j0, lo, hi) & rp->valid[0], range_mask(j0 + 32, lo, hi) & rp->valid[1]};
+        const float kc[4] = {fmaxf(kc4.x * back, SCALE_MIN), fmaxf(kc4.y * back, SCALE_MIN),
+                             fmaxf(kc4.z * back, SCALE_MIN), fmaxf(kc4.w * back, SCALE_MIN)};
+        const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, wl[4] = {wl4.x, wl4.y, wl4.z, wl4.w};
+        tmem_ld_wait();
+        if ((vb[0] & vb[1]) != 0xFFFFFFFFu) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) tmem_ld16(tS + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
-          tmem_ld_wait();
-          if (!clear) {
-#pragma unroll
-            for (int j = 0; j < 64; j++)
-              if (!((vb[2 * c + (j >> 5)] >> (j & 31)) & 1u)) sv[j] = 0xFF800000u;
-          }
-        };
+          for (int j = 0; j < TILE; j++)
+            if (!((vb[j >> 5] >> (j & 31)) & 1u)) sv[j] = 0xFF800000u;  // -inf
+        }
         float mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
 #pragma unroll
-        for (int c = 1; c >= 0; c--) {
-          load_scores(c);
+        for (int q = 0; q < 4; q++) {
+          float sx = fmaxf(__uint_as_float(sv[16 * q]), __uint_as_float(sv[16 * q + 1]));
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            float sx = fmaxf(__uint_as_float(sv[16 * q]), __uint_as_float(sv[16 * q + 1]));
-#pragma unroll
-            for (int j = 2; j < 16; j += 2)
-              sx = fmax3(sx, __uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1]));
-            const float zx = sx * fmaxf(rp->kc[4 * c + q] * back, SCALE_MIN);
-            mz = fmaxf(mz, zx);
-            mw = fmaxf(mw, zx + rp->lv[4 * c + q]);
-          }
+          for (int j = 2; j < 16; j += 2)
+            sx = fmax3(sx, __uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1]));
+          const float zx = sx * kc[q];
+          mz = fmaxf(mz, zx);
+          mw = fmaxf(mw, zx + lv[q]);
         }
         const float m2 = fmaxf(m, mz);
         l *= m2 == m ? 1.f : ex2_ftz(m - m2);
@@ -675,61 +691,63 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float M2 = mw > M + P_LAZY ? mw : M;
         const float al = M2 == M || M == -INFINITY ? 1.f : ex2_ftz(M - M2);
         M = M2;
-        // O is stable: S of this step was issued behind the completed PV of the last one
         if (__any_sync(0xffffffffu, al != 1.f)) {
+          // rescale O, once PV of the last step is done with it (rows without a reference yet are
+          // in their first step or have an O of zeros)
+          if (k > 0) {
+            ok = mbar_wait(&o_done[t], (n & 1) ^ 1, p.limit, s_abort);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+          }
 #pragma unroll
-          for (int c = 0; c < D / 64; c++) {
+          for (int c = 0; c < D / 32; c++) {
+            uint32_t r[32];
 #pragma unroll
-            for (int q = 0; q < 4; q++) tmem_ld16(tO + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
+            for (int q = 0; q < 2; q++) tmem_ld16(tO + 32 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 64; j++) sv[j] = __float_as_uint(__uint_as_float(sv[j]) * al);
+            for (int j = 0; j < 32; j++) r[j] = __float_as_uint(__uint_as_float(r[j]) * al);
 #pragma unroll
-            for (int q = 0; q < 4; q++) tmem_st16(tO + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
+            for (int q = 0; q < 2; q++) tmem_st16(tO + 32 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
           }
-          load_scores(0);
         }
         const float Mu = M == -INFINITY ? 0.f : M, mu = m == -INFINITY ? 0.f : m;
-        // P over the first half of S: columns 64 c .. + 63 go to columns 32 c .. + 31, whose scores
-        // are in registers (c = 0) or used (c = 1)
+        // P over the first half of its S, whose scores are in registers
         float lr = 0.f;
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-          if (c == 1) load_scores(1);
+          uint32_t pk[16];
 #pragma unroll
-          for (int hf = 0; hf < 2; hf++) {
-            uint32_t pk[16];
+          for (int q = 0; q < 2; q++) {
+            const int gq = 2 * c + q;
+            const float add = lv[gq] - Mu + P_OFF;
+            const unsigned long long c2 = f2_make(kc[gq], kc[gq]), a2 = f2_make(add, add);
+            unsigned long long g = 0ull;
 #pragma unroll
-            for (int q = 0; q < 2; q++) {
-              const int gq = 4 * c + 2 * hf + q;
-              const float cc = fmaxf(rp->kc[gq] * back, SCALE_MIN), add = rp->lv[gq] - Mu + P_OFF;
-              const unsigned long long c2 = f2_make(cc, cc), a2 = f2_make(add, add);
-              unsigned long long g = 0ull;
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const int e = 32 * hf + 16 * q + j;
-                const unsigned long long x =
-                    f2_fma(f2_make(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, a2);
-                const float e0 = ex2_ftz(f2_lo(x)), e1 = ex2_ftz(f2_hi(x));
-                g = f2_add(g, f2_make(e0, e1));
-                pk[8 * q + (j >> 1)] = half2_of(e0, e1);
-              }
-              lr = fmaf(f2_lo(g) + f2_hi(g), rp->wl[gq], lr);
+            for (int j = 0; j < 16; j += 2) {
+              const int e = 16 * gq + j;
+              const unsigned long long x = f2_fma(f2_make(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, a2);
+              const float e0 = ex2_ftz(f2_lo(x)), e1 = ex2_ftz(f2_hi(x));
+              g = f2_add(g, f2_make(e0, e1));
+              pk[8 * q + (j >> 1)] = half2_of(e0, e1);
             }
-            tmem_st16(tS + 32 * c + 16 * hf, pk);
+            lr = fmaf(f2_lo(g) + f2_hi(g), wl[gq], lr);
           }
+          tmem_st16(tSn + 16 * c, pk);
         }
-        l = fmaf(lr, ex2_ftz(Mu - P_OFF - rp->lvref - mu), l);
+        l = fmaf(lr, ex2_ftz(Mu - P_OFF - lvref - mu), l);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[t]);
+        mbar_arrive(&p_full[2 * t + (n & 1)]);
       }
       if (ok && steps > 0) {
         ok = mbar_wait(&o_done[t], (step + steps - 1) & 1, p.limit, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        if (ok) look(rg + (pair ? n - 1 : 2 * (steps - 1) + t),
-                     jfirst + (pair ? n - 1 : 2 * (steps - 1) + t) * TILE);
+        for (int k = max(0, steps - 2); ok && k < steps; k++) {
+          const int rr = pair ? k : 2 * k + t;
+          look(rg + rr, jfirst + rr * TILE);
+        }
       }
       if (sick) l = NAN;
       if (!ok) {
