@@ -39,6 +39,9 @@ namespace {
 constexpr int TILE = 64;       // KV rows per round
 constexpr int ITEM = ROWS_ITEM;  // query rows per item
 constexpr int THREADS = 16 * 32;
+// What an item costs beyond its rounds (Q, pipeline fill, output), in rounds: the blocks' shares
+// count it, or those of a prompt's first tiles (few rounds, many items) take twice as long.
+constexpr int ITEM_COST = 4;
 constexpr int PRING = 16;      // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
@@ -126,9 +129,12 @@ struct Walk {
   int rd, count;           // this block's rounds of the item: rd .. rd + count - 1 of nt
   long long left;
 };
-__device__ __forceinline__ void walk_set(const Params& p, Walk& w) {
-  w.count = (int)min((long long)(w.nt - w.rd), w.left);
-  w.left -= w.count;
+// The units of an item are ITEM_COST + rounds; `at`: this block's first of them.
+__device__ __forceinline__ void walk_set(Walk& w, int at) {
+  const int n = (int)min((long long)(ITEM_COST + w.nt - at), w.left);  // this block's units
+  w.rd = max(0, at - ITEM_COST);
+  w.count = max(0, at + n - ITEM_COST) - w.rd;
+  w.left -= n;
 }
 __device__ __forceinline__ bool walk_first(const Params& p, const Share& s, int b, int tile, Walk& w) {
   w.left = s.u1 - s.u0;
@@ -137,9 +143,8 @@ __device__ __forceinline__ bool walk_first(const Params& p, const Share& s, int 
   w.tile = tile;
   w.r = load_req(p, b, false);
   w.nt = rounds_of(p, w.r, tile, &w.j0);
-  w.g = (int)s.rem / w.nt;
-  w.rd = (int)s.rem - w.g * w.nt;
-  walk_set(p, w);
+  w.g = (int)s.rem / (ITEM_COST + w.nt);
+  walk_set(w, (int)s.rem - w.g * (ITEM_COST + w.nt));
   return true;
 }
 __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
@@ -153,8 +158,7 @@ __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
     }
     w.nt = rounds_of(p, w.r, w.tile, &w.j0);
   }
-  w.rd = 0;
-  walk_set(p, w);
+  walk_set(w, 0);
   return true;
 }
 // What the roles are told of an item, in shared memory, written by the walking warp.
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   pdl_enter();
   tc_fence_before();
-  // Units are rounds; the entries that share them are all tiles of all requests, so that no
+  // Units are rounds and ITEM_COST an item; the entries that share them are all tiles of all requests, so that no
   // thread has a long prompt to itself.  s_first (in memory that Q will take): each request's
   // first tile.
   long long* scratch = reinterpret_cast<long long*>(sm + C::SCRATCH);
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const Share share = find_share<THREADS>((int)all_tiles, blockIdx.x, p.n_blocks, scratch, [&](int e) {
     int j0;
     tile_at(e);
-    return (long long)rounds_of(p, at_r, e - s_first[at_b], &j0) * p.a.kv.Hkv;
+    return (long long)(ITEM_COST + rounds_of(p, at_r, e - s_first[at_b], &j0)) * p.a.kv.Hkv;
   });
   at_b = -1;
   const int b0 = share.u1 > share.u0 ? tile_at(share.e) : 0;
@@ -532,6 +536,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       Walk w;
       bool more = walk_first(p, share, b0, tile0, w), ok = true;
       Meta* m = p.meta + blockIdx.x;
+      // (parts are told apart by rounds: an item's first part is with the block of its first round)
       m->ends = w.rd > 0 && w.rd + w.count == w.nt;
       m->first = share.u0 - w.rd;
       m->tot = share.tot;
@@ -542,6 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (uint32_t it = 0; ok; it++) {
         if (it >= IRING) ok = mbar_wait(&i_empty[it % IRING], ((it / IRING) & 1) ^ 1, p.limit, s_abort);
         if (!ok) break;
+        while (more && w.count == 0) more = walk_next(p, w);  // shares that end before the first round
         Item im = {};
         if (more) {
           im.count = w.count;
@@ -592,7 +598,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       int hi, lo;
       size_t orow;
       int head;
-      const __nv_bfloat16* qrow;
       {
         const int qr = im->row0 + (valid ? irow : 0), qi = p.by_G.div(qr);
         const Req r = {0, im->c0, im->len, im->qs};
@@ -600,36 +605,46 @@ __global__ void __launch_bounds__(THREADS, 1)
         lo = valid ? vis_lo(p, r, qi) : 0;
         head = im->g * p.G + qr - qi * p.G;
         orow = (size_t)(r.c0 + qi) * p.a.H + head;
-        qrow = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(r.c0 + qi) * p.a.q_stride + head * D;
       }
-      // Q row -> fp16 with its exponent taken out (in single mode group 1 only needs the factor)
-      float back;
+      // Q rows -> fp16 with their exponents taken out, D / 8 lanes a row (in single mode group 1
+      // only needs the factors)
+      float back = 1.f;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(qrow);
-        uint4 x[D / 8];
-        float am = 0.f;
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
+        const int wrow = (pair ? t * 128 : 0) + (warp & 3) * 32, sub = lane / LPR, piece = lane % LPR;
+        uint4 x[32 / RPI];
 #pragma unroll
-        for (int c = 0; c < D / 8; c++) {
-          x[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+        for (int i = 0; i < 32 / RPI; i++) {
+          const int ir = wrow + i * RPI + sub;
+          const int qr = im->row0 + min(ir, rows - 1), qi = p.by_G.div(qr);
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(im->c0 + qi) * p.a.q_stride +
+                                     (im->g * p.G + qr - qi * p.G) * D;
+          x[i] = ir < rows ? __ldg(reinterpret_cast<const uint4*>(src) + piece) : make_uint4(0, 0, 0, 0);
+        }
+        uint8_t* qt = sm + t * C::QT;
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; i++) {
+          uint32_t a[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          float am = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; k++)
             am = fmax3(am, fabsf(__uint_as_float(a[k] << 16)), fabsf(__uint_as_float(a[k] & 0xFFFF0000u)));
-        }
-        const float f = row_factor(am, &back);
-        if (pair || t == 0) {
-          uint8_t* qt = sm + t * C::QT;
 #pragma unroll
-          for (int c = 0; c < D / 8; c++) {
-            uint32_t a[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          for (int o = 1; o < LPR; o <<= 1) am = fmaxf(am, __shfl_xor_sync(~0u, am, o));
+          float bk;
+          const float f = row_factor(am, &bk);
+          const float mine = __shfl_sync(~0u, bk, (lane % RPI) * LPR);
+          if (lane / RPI == i) back = mine;  // (lane r owns row r of the warp)
+          if (pair || t == 0) {
+            const int r = (warp & 3) * 32 + i * RPI + sub;
 #pragma unroll
             for (int k = 0; k < 4; k++)
               a[k] = half2_of(__uint_as_float(a[k] << 16) * f, __uint_as_float(a[k] & 0xFFFF0000u) * f);
-            *reinterpret_cast<uint4*>(qt + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(qt + (piece >> 3) * 16384 + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
                 make_uint4(a[0], a[1], a[2], a[3]);
           }
-          fence_proxy_async_smem();
         }
+        fence_proxy_async_smem();
         mbar_arrive(&q_full[t]);
       }
       const int steps = pair ? n : (n + 1 - t) / 2;
@@ -795,18 +810,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           *reinterpret_cast<float4*>(pp + irow * 4) = make_float4(m, M, l, 0.f);
         }
+        // 64 dimensions at a time: a row's values go through shared memory (the row's own place,
+        // where Q or the exchange was), so that the warp writes whole rows
+        const int wr = (warp & 3) * 32;
+        uint8_t* stage = sm + (pair ? t * C::QT : 0);
+        const uint32_t pitch = pair ? D * 2 : D * 4;
 #pragma unroll
-        for (int q = 0; q < D / 16; q++) {
-          uint32_t r16[16];
-          tmem_ld16(tO + q * 16, r16);
+        for (int c = 0; c < D / 64; c++) {
+          float x[64];
+#pragma unroll
+          for (int q = 0; q < 4; q++)
+            tmem_ld16(tO + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(&x[16 * q])));
           tmem_ld_wait();
-          float x[16];
 #pragma unroll
-          for (int j = 0; j < 16; j++) x[j] = mine == 0.f ? 0.f : __uint_as_float(r16[j]) * mine;
+          for (int j = 0; j < 64; j++) x[j] = mine == 0.f ? 0.f : x[j] * mine;
           if (other != 0.f) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(ex + row * D + (((q * 4 + (j >> 2)) ^ (row & 7)) << 2));
+            for (int j = 0; j < 64; j += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(ex + row * D + (((c * 16 + (j >> 2)) ^ (row & 7)) << 2));
               x[j] = fmaf(y.x, other, x[j]);
               x[j + 1] = fmaf(y.y, other, x[j + 1]);
               x[j + 2] = fmaf(y.z, other, x[j + 2]);
@@ -814,20 +835,47 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           if (whole) {
-            if (valid) {
-              uint32_t h[8];
+            // bf16: 8 pieces of 16 bytes a row; lanes 8 i .. write row 4 k + i
+            uint8_t* mine8 = stage + row * pitch + (pair ? 0 : c * 256);
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) h[j >> 1] = f == 0.f ? 0u : bf16x2_of(x[j] * f, x[j + 1] * f);
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + q * 16);
-              dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-              dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+            for (int e = 0; e < 8; e++) {
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; k++) h[k] = f == 0.f ? 0u : bf16x2_of(x[8 * e + 2 * k] * f, x[8 * e + 2 * k + 1] * f);
+              *reinterpret_cast<uint4*>(mine8 + ((e ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
-          } else if (valid) {
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; j += 4)
-              *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)irow * D + q * 16 + j) =
-                  make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            for (int k = 0; k < 8; k++) {
+              const int r = 4 * k + (lane >> 3), e = lane & 7;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + (wr + r) * pitch + (pair ? 0 : c * 256) +
+                                                              ((e ^ (r & 7)) << 4));
+              const size_t to = __shfl_sync(~0u, (unsigned long long)orow, r);
+              if (__shfl_sync(~0u, (int)valid, r))
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + to * D + c * 64 + e * 8) = v;
+            }
+          } else {
+            // fp32: 64 values a row, in two halves of 8 pieces
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              uint8_t* mine8 = stage + row * pitch + (pair ? 0 : c * 256);
+#pragma unroll
+              for (int e = 0; e < 8; e++)
+                *reinterpret_cast<float4*>(mine8 + ((e ^ (row & 7)) << 4)) =
+                    make_float4(x[32 * h + 4 * e], x[32 * h + 4 * e + 1], x[32 * h + 4 * e + 2], x[32 * h + 4 * e + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; k++) {
+                const int r = 4 * k + (lane >> 3), e = lane & 7;
+                const float4 v = *reinterpret_cast<const float4*>(stage + (wr + r) * pitch + (pair ? 0 : c * 256) +
+                                                                  ((e ^ (r & 7)) << 4));
+                if (__shfl_sync(~0u, (int)valid, r))
+                  *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)(irow - lane + r) * D + c * 64 + 32 * h + e * 4) = v;
+              }
+              __syncwarp();
+            }
           }
+          __syncwarp();
         }
       }
       // O is read and the exchange buffer is free before the next item's Q
