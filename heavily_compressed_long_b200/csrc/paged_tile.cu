@@ -41,7 +41,7 @@ constexpr int ITEM = ROWS_ITEM;  // query rows per item
 constexpr int THREADS = 16 * 32;
 // What an item costs beyond its rounds (Q, pipeline fill, output), in rounds: the blocks' shares
 // count it, or those of a prompt's first tiles (few rounds, many items) take twice as long.
-constexpr int ITEM_COST = 4;
+constexpr int ITEM_COST = 13;
 constexpr int PRING = 16;      // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
