@@ -218,34 +218,45 @@ def hcl_lse_merge(o_parts, lse_parts, out, lse_out=None, sink=None, stream=None)
                               _ptr(lse_out), _stream(stream)))
 
 
-def _i32(t, name, n=None):
-    """The address of a contiguous int32 tensor on the current device (n: its element count)."""
-    if t.dtype != torch.int32 or not t.is_contiguous():
+# The paged cache's calls are made once per layer and step, on small batches too, so their checks
+# are kept to a few attribute reads per tensor.
+
+
+def _stream_on(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _i32(t, name, dev, n=None):
+    """The address of a contiguous int32 tensor on device `dev` (n: its element count)."""
+    if t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
-    return _here(t, name)
+    return t.data_ptr()
 
 
-def _here(t, name):
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+def _dense(t, name, dev, dtype, shape):
+    """The address of a contiguous tensor of the given type and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)}")
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
     return t.data_ptr()
 
 
-def _rows(t, name, heads, d):
+def _rows(t, name, dev, heads, d):
     """(address, token stride in elements) of bf16 rows [T, heads, d] whose heads lie together:
     a whole tensor, or a slice of wider rows such as a fused projection's output."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, d):
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, d):
         raise ValueError(f"{name} must be bf16 [T, {heads}, {d}]")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != d):
         raise ValueError(f"{name}: the heads of a token must lie together")
-    return _here(t, name), (s[0] if t.shape[0] > 1 else max(s[0], heads * d))
-
-
-def _status(status):
-    return None if status is None else _i32(status, "status")
+    return t.data_ptr(), (s[0] if t.shape[0] > 1 else max(s[0], heads * d))
 
 
 class PagedKV:
@@ -255,20 +266,19 @@ class PagedKV:
     def __init__(self, k, k_scale, v=None, v_scale=None):
         if (v is None) != (v_scale is None):
             raise ValueError("v and v_scale go together")
+        if k.dim() != 4:
+            raise ValueError("k must be codes [n_pages, Hkv, page, d]")
         n, Hkv, page, d = k.shape
+        dev = torch.cuda.current_device()
+        ptr = []
         for name, codes, scale in (("k", k, k_scale), ("v", v, v_scale)):
-            if codes is None:
-                continue
-            if codes.dtype != torch.uint8 or codes.shape != k.shape or not codes.is_contiguous():
-                raise ValueError(f"{name} must be contiguous uint8 codes [n_pages, Hkv, page, d]")
-            if scale.dtype != torch.float32 or scale.shape != (n, Hkv) or not scale.is_contiguous():
-                raise ValueError(f"{name}_scale must be contiguous fp32 [n_pages, Hkv]")
+            ptr.append(None if codes is None else _dense(codes, name, dev, torch.uint8, k.shape))
+            ptr.append(None if codes is None else
+                       _dense(scale, name + "_scale", dev, torch.float32, (n, Hkv)))
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
-        self.n_pages, self.Hkv, self.page, self.d = n, Hkv, page, d
-        planes = [None if t is None else _here(t, "the store") for t in (k, v, k_scale, v_scale)]
-        self._c = hcl_paged_kv_t(page, n, Hkv, d, *planes)
+        self.n_pages, self.Hkv, self.page, self.d, self.dev = n, Hkv, page, d, dev
+        self._c = hcl_paged_kv_t(page, n, Hkv, d, ptr[0], ptr[2], ptr[1], ptr[3])
         self._ref = ctypes.byref(self._c)
-        self.device = k.device
 
     @classmethod
     def empty(cls, n_pages, Hkv, page, d, shared=False, device="cuda"):
@@ -278,8 +288,8 @@ class PagedKV:
                     torch.ones(n_pages, Hkv, dtype=torch.float32, device=device))
         return cls(*plane()) if shared else cls(*plane(), *plane())
 
-    def ref(self):
-        if self.device.index != torch.cuda.current_device():
+    def ref(self, dev):
+        if self.dev != dev:
             raise ValueError("the store must be on the current CUDA device")
         return self._ref
 
@@ -291,23 +301,26 @@ def hcl_page_plan(keep, new_len, seq_len, table, free_list, n_free, page, cu_new
     [B + 1]; pos, slot int32 [T]."""
     B, max_pages = table.shape
     T = slot.numel()
-    check(lib().hcl_page_plan(_i32(keep, "keep", B), _i32(new_len, "new_len", B), B, page,
-                              _i32(seq_len, "seq_len", B), _i32(table, "table"), max_pages,
-                              _i32(free_list, "free_list"), free_list.numel(),
-                              _i32(n_free, "n_free", 1), T, _i32(cu_new, "cu_new", B + 1),
-                              _i32(pos, "pos", T), _i32(slot, "slot"), _status(status),
-                              _stream(stream)))
+    dev = torch.cuda.current_device()
+    check(lib().hcl_page_plan(
+        _i32(keep, "keep", dev, B), _i32(new_len, "new_len", dev, B), B, page,
+        _i32(seq_len, "seq_len", dev, B), _i32(table, "table", dev), max_pages,
+        _i32(free_list, "free_list", dev), free_list.numel(), _i32(n_free, "n_free", dev, 1), T,
+        _i32(cu_new, "cu_new", dev, B + 1), _i32(pos, "pos", dev, T), _i32(slot, "slot", dev),
+        None if status is None else _i32(status, "status", dev), _stream_on(stream, dev)))
 
 
 def hcl_paged_write(k_new, v_new, slot, store: PagedKV, status=None, stream=None):
     """Quantise new rows (bf16 [T, Hkv, d]; v_new None for a store without v) into their slots."""
     T = slot.numel()
-    k, ks = _rows(k_new, "k_new", store.Hkv, store.d)
-    v, vs = (None, 0) if v_new is None else _rows(v_new, "v_new", store.Hkv, store.d)
+    dev = torch.cuda.current_device()
+    k, ks = _rows(k_new, "k_new", dev, store.Hkv, store.d)
+    v, vs = (None, 0) if v_new is None else _rows(v_new, "v_new", dev, store.Hkv, store.d)
     if k_new.shape[0] != T or (v_new is not None and v_new.shape[0] != T):
         raise ValueError("k_new, v_new and slot must have as many rows")
-    check(lib().hcl_paged_write(k, ks, v, vs, _i32(slot, "slot"), T, store.ref(), _status(status),
-                                _stream(stream)))
+    check(lib().hcl_paged_write(k, ks, v, vs, _i32(slot, "slot", dev), T, store.ref(dev),
+                                None if status is None else _i32(status, "status", dev),
+                                _stream_on(stream, dev)))
 
 
 def paged_attn_workspace_bytes(T, H, Hkv, d):
@@ -320,28 +333,25 @@ def hcl_paged_attn(q, cu_q, q_start, store: PagedKV, table, kv_len, out, lse=Non
     the first at position q_start[b]) over the pages that table int32 [B, max_pages] lists."""
     T, H, d = q.shape
     B, max_pages = table.shape
-    qp, qs = _rows(q, "q", H, store.d)
-    if out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be contiguous bf16 of q's shape")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [T, H]")
-    if sink is not None and (sink.dtype != torch.float32 or sink.shape != (H,) or not sink.is_contiguous()):
-        raise ValueError("sink must be contiguous fp32 [H]")
+    dev = torch.cuda.current_device()
+    qp, qs = _rows(q, "q", dev, H, store.d)
     if ws is None:
         need = paged_attn_workspace_bytes(T, H, store.Hkv, d)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
             if stream is not None:
                 ws.record_stream(stream)
-    check(lib().hcl_paged_attn(qp, qs, T, H, _i32(cu_q, "cu_q", B + 1), _i32(q_start, "q_start", B), B,
-                               store.ref(), _i32(table, "table"), max_pages,
-                               _i32(kv_len, "kv_len", B), T if max_q is None else max_q, m, W,
-                               1.0 / math.sqrt(d) if scale is None else scale,
-                               None if sink is None else _here(sink, "sink"), _here(out, "out"),
-                               None if lse is None else _here(lse, "lse"),
-                               None if ws is None else _here(ws, "ws"),
-                               0 if ws is None else ws.numel() * ws.element_size(), _status(status),
-                               _stream(stream)))
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous, on the current CUDA device")
+    check(lib().hcl_paged_attn(
+        qp, qs, T, H, _i32(cu_q, "cu_q", dev, B + 1), _i32(q_start, "q_start", dev, B), B,
+        store.ref(dev), _i32(table, "table", dev), max_pages, _i32(kv_len, "kv_len", dev, B),
+        T if max_q is None else max_q, m, W, 1.0 / math.sqrt(d) if scale is None else scale,
+        None if sink is None else _dense(sink, "sink", dev, torch.float32, (H,)),
+        _dense(out, "out", dev, torch.bfloat16, q.shape),
+        None if lse is None else _dense(lse, "lse", dev, torch.float32, (T, H)),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+        None if status is None else _i32(status, "status", dev), _stream_on(stream, dev)))
     return out
 
 

@@ -345,8 +345,10 @@ int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 
 
 hcl_status_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st) {
   const int smem = (4 * a.B + 3) * 4;
-  hcl_status_t e = set_kernel_attrs(reinterpret_cast<const void*>(page_plan_kernel), smem, false);
-  if (e != HCL_OK) return e;
+  if (smem > 48 * 1024) {
+    hcl_status_t e = set_kernel_attrs(reinterpret_cast<const void*>(page_plan_kernel), smem, false);
+    if (e != HCL_OK) return e;
+  }
   const int work = std::max(a.T, a.B);
   const int blocks = work <= 4096 ? 1 : work <= 16384 ? 4 : 8;
   return check_cuda(launch_pdl(page_plan_kernel, dim3(blocks), dim3(PP_THREADS), (size_t)smem, st, blocks,
