@@ -4,10 +4,12 @@
 // Block: one producer warp and four consumer warps, two blocks per SM.  A unit is 64 KV rows of
 // one request and KV head.  The producer copies its codes with TMA (one box per page, or per 64
 // rows of a longer page) into a ring of swizzled stages and its page scales with 4-byte
-// asynchronous copies that complete on the same mbarrier; the page ids are read one unit ahead.
-// Consumer warp w owns rows 16w .. 16w + 15 of every unit and its own running softmax, so warps
-// never wait for one another inside an item:
-//   S (16 query rows x 16 KV rows) by m16n8k16 fp16 MMAs; the K fragments come from ldmatrix on
+// asynchronous copies that complete on the same mbarrier; page ids are read eight units at a time,
+// eight ahead.  Consumer warps 0, 1 take the even units and 2, 3 the odd ones, each 32 rows and
+// its own running softmax, so warps never wait for one another inside an item.  (With 16 rows of
+// every unit to each warp the chain from load to store, not the bytes, set the pace: 300 us for
+// 1.37 GB; with 32, 265 us; 64 gain nothing more.)
+//   S (16 query rows x 32 KV rows) by m16n8k16 fp16 MMAs; the K fragments come from ldmatrix on
 //   the codes (a 16-byte piece of a row is one k-step, its dimensions taken in the order that
 //   gives each thread four neighbouring codes; Q is laid out alike) and a conversion to fp16;
 //   O += P V the same way from transposed ldmatrix on pairs of codes (even and odd dimensions
@@ -23,7 +25,9 @@ namespace {
 
 constexpr int NW = 4;                  // consumer warps
 constexpr int THREADS = (NW + 1) * 32;
-constexpr int TILE = 16 * NW;          // KV rows per unit
+constexpr int TILE = 64;               // KV rows per unit
+constexpr int NG = 2;                  // groups of 16 rows (never more than a page) per warp and unit
+constexpr int WPT = TILE / (16 * NG);  // warps per unit
 
 template <int D, bool SHARED>
 struct Cfg {
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; i++) {
       mbar_init(&full[i], 1 + 32);
-      mbar_init(&empty[i], NW);
+      mbar_init(&empty[i], WPT);
     }
     *s_abort = 0;
     fence_barrier_init();
@@ -160,15 +164,19 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int box = min(p.a.kv.page, TILE);  // rows of a box
     uint32_t it = 0;
     bool fault = false, ok = true;
-    // the page of this lane's 16-row group (lanes 0..3) in a tile; -1 behind the rows held
-    auto page_of = [&](const Walk& v, int i) {
-      const int t = (v.t0 + v.tile + i) * TILE + (lane & 3) * 16;
-      return t < v.r.len ? __ldg(p.a.table + (size_t)v.b * p.a.max_pages + (t >> p.sh)) : -2;
+    // pages of the 32 groups from tile i of this part on; -2 behind the rows held
+    auto pages_at = [&](int i) {
+      const int t = (w.t0 + w.tile + i) * TILE + lane * 16;
+      return i < w.count && t < w.r.len ? __ldg(p.a.table + (size_t)w.b * p.a.max_pages + (t >> p.sh)) : -2;
     };
     do {
-      int id = page_of(w, 0);
+      int ids = -2, ids_next = pages_at(0);
       for (int i = 0; i < w.count && ok; i++, it++) {
-        const int next = i + 1 < w.count ? page_of(w, i + 1) : -2;
+        if ((i & 7) == 0) {
+          ids = ids_next;
+          ids_next = pages_at(i + 8);
+        }
+        const int id = __shfl_sync(~0u, ids, (i & 7) * 4 + (lane & 3));
         const int st = it % C::STAGES;
         if (it >= C::STAGES)
           ok = __all_sync(~0u, mbar_wait(&empty[st], ((it / C::STAGES) & 1) ^ 1, p.limit, s_abort));
@@ -198,7 +206,6 @@ __global__ void __launch_bounds__(THREADS, 2)
                          "l"(p.a.kv.v_scale + pg) : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[st])) : "memory");
-        id = next;
       }
     } while (ok && walk_next(p, w));
     if (!ok) {
@@ -261,108 +268,132 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
       for (int k = 0; k < 8; k++) o[c][k] = 0.f;
+    const int rows0 = (warp % WPT) * 16 * NG;  // this warp's rows of a tile
     float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lvref = -INFINITY;
 
     for (int i = 0; i < w.count; i++, it++) {
+      if (it % (NW / WPT) != warp / WPT) continue;
       const int st = it % C::STAGES;
       ok = mbar_wait(&full[st], (it / C::STAGES) & 1, p.limit, s_abort);
       ok = __all_sync(~0u, ok);
       if (!ok) break;
-      const int j0 = (w.t0 + w.tile + i) * TILE + warp * 16;
-      const float ks = s_scale[st * 8 + warp];
-      if (j0 < any_hi && j0 + 16 > any_lo && ks > 0.f) {
-        const uint32_t kb = smem_u32(sm + st * C::STAGE) + warp * 16 * D;
+      const int j0 = (w.t0 + w.tile + i) * TILE + rows0;
+      float ks[NG];
+#pragma unroll
+      for (int g = 0; g < NG; g++) ks[g] = s_scale[st * 8 + (rows0 >> 4) + g];
+      if (j0 < any_hi && j0 + 16 * NG > any_lo) {
+        const uint32_t kb = smem_u32(sm + st * C::STAGE) + rows0 * D;
         const uint32_t vb = kb + (SHARED ? 0 : C::PLANE);
         // S
-        float s[2][2][4];  // [n-tile][chain]
+        float s[2 * NG][4];  // [n-tile]
 #pragma unroll
-        for (int n = 0; n < 2; n++)
+        for (int n = 0; n < 2 * NG; n++)
 #pragma unroll
-          for (int c = 0; c < 2; c++)
+          for (int k = 0; k < 4; k++) s[n][k] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; k++) s[n][c][k] = 0.f;
+        for (int q = 0; q < C::PIECES / 4; q++)
 #pragma unroll
-        for (int n = 0; n < 2; n++)
-#pragma unroll
-          for (int q = 0; q < C::PIECES / 4; q++) {
+          for (int n = 0; n < 2 * NG; n++) {
             uint32_t r[4];
             ldsm4(kb + piece<D>(n * 8 + (lane & 7), q * 4 + (lane >> 3)), r);
 #pragma unroll
             for (int c = 0; c < 4; c++)
-              mma16816(s[n][c & 1], qf[q * 4 + c], half2_of_codes(uint16_t(r[c])), half2_of_codes(uint16_t(r[c] >> 16)));
+              mma16816(s[n], qf[q * 4 + c], half2_of_codes(uint16_t(r[c])), half2_of_codes(uint16_t(r[c] >> 16)));
           }
-        float z[2][4];  // [row half][columns 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4]
+        float z[NG][2][4];  // [group][row half][columns 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4]
 #pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-          for (int n = 0; n < 2; n++)
-#pragma unroll
-            for (int k = 0; k < 2; k++) z[h][2 * n + k] = s[n][0][2 * h + k] + s[n][1][2 * h + k];
-        uint32_t poison = 0;
-        if (j0 < all_lo || j0 + 16 > all_hi) {
-          // some row does not see some of these KV rows
+        for (int g = 0; g < NG; g++)
 #pragma unroll
           for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-              const int j = j0 + (k >> 1) * 8 + 2 * t4 + (k & 1);
-              if (j < lo_r[h] || j >= hi_r[h]) z[h][k] = -INFINITY;
-            }
-          // NaN codes among the values would reach the rows that do not see them (0 * NaN), and
-          // rows behind the last hold anything: they become 0, and `poison` says which KV rows
-          // had one
-          __syncwarp();
-          uint8_t* vp = sm + st * C::STAGE + (SHARED ? 0 : C::PLANE) + warp * 16 * D;
+            for (int k = 0; k < 4; k++)  // (a group without a page is left out)
+              z[g][h][k] = ks[g] > 0.f ? s[2 * g + (k >> 1)][2 * h + (k & 1)] : -INFINITY;
+        uint32_t poison = 0;  // a bit for each of the KV rows
+        static_assert(16 * NG <= 32, "poison");
+        if (j0 < all_lo || j0 + 16 * NG > all_hi || !(ks[0] > 0.f) || !(ks[NG - 1] > 0.f)) {
+          // some row does not see some of these KV rows
 #pragma unroll
-          for (int e = lane; e < 16 * C::PIECES; e += 32) {
-            uint4* at = reinterpret_cast<uint4*>(vp + e * 16);
-            uint4 v = *at;
-            const uint4 n4 = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
-            if (n4.x | n4.y | n4.z | n4.w) {
-              *at = make_uint4(v.x & ~n4.x, v.y & ~n4.y, v.z & ~n4.z, v.w & ~n4.w);
-              poison |= 1u << (e / C::PIECES);
+          for (int g = 0; g < NG; g++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+              for (int k = 0; k < 4; k++) {
+                const int j = j0 + g * 16 + (k >> 1) * 8 + 2 * t4 + (k & 1);
+                if (j < lo_r[h] || j >= hi_r[h]) z[g][h][k] = -INFINITY;
+              }
+          // NaN codes among the values would reach the rows that do not see them (0 * NaN), and
+          // rows behind the last (or of no page) hold anything: they become 0, and `poison` says
+          // which KV rows had one
+          __syncwarp();
+          uint8_t* vp = sm + st * C::STAGE + (SHARED ? 0 : C::PLANE) + rows0 * D;
+#pragma unroll
+          for (int g = 0; g < NG; g++)
+#pragma unroll
+            for (int i = 0; i < C::PIECES / 2; i++) {
+              const int e = i * 32 + lane;  // piece of the group
+              uint4* at = reinterpret_cast<uint4*>(vp + g * 16 * D + e * 16);
+              const uint4 v = *at;
+              const uint4 n4 = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
+              if (n4.x | n4.y | n4.z | n4.w) {
+                *at = make_uint4(v.x & ~n4.x, v.y & ~n4.y, v.z & ~n4.z, v.w & ~n4.w);
+                if (ks[g] > 0.f) poison |= 1u << (g * 16 + e / C::PIECES);
+              }
             }
-          }
           poison = __reduce_or_sync(~0u, poison);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        const float lv_page = log2_scale(SHARED ? ks : s_scale[st * 8 + 4 + warp]);
-        lvref = fmaxf(lvref, lv_page);
-        const float lv = fmaxf(lv_page, lvref - LV_SPAN);
-        const float wl = ex2_ftz(lvref - lv);
-        const float kc = fmaxf(ks, SCALE_MIN) * p.scale2;
+        float lv[NG], wl[NG], kc[NG];
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          lv[g] = log2_scale(SHARED ? ks[g] : s_scale[st * 8 + 4 + (rows0 >> 4) + g]);
+          if (ks[g] > 0.f) lvref = fmaxf(lvref, lv[g]);
+          kc[g] = fmaxf(ks[g], SCALE_MIN) * p.scale2;
+        }
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          lv[g] = ks[g] > 0.f ? fmaxf(lv[g], lvref - LV_SPAN) : lvref;
+          wl[g] = ks[g] > 0.f ? ex2_ftz(lvref - lv[g]) : 0.f;
+        }
         float al[2];
-        uint32_t pf[4];
+        uint32_t pf[NG][4];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const float c = fmaxf(kc * back[h], SCALE_MIN);
-          float mx = fmaxf(fmaxf(z[h][0], z[h][1]), fmaxf(z[h][2], z[h][3]));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-          mx *= c;  // -inf when nothing is seen
-          const float m2 = fmaxf(m[h], mx);
+          float c[NG], mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            c[g] = fmaxf(kc[g] * back[h], SCALE_MIN);
+            const float x = fmax3(fmaxf(z[g][h][0], z[g][h][1]), z[g][h][2], z[g][h][3]) * c[g];
+            mz = fmaxf(mz, x);
+            mw = fmaxf(mw, x + lv[g]);
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            mz = fmaxf(mz, __shfl_xor_sync(~0u, mz, o));
+            mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, o));
+          }
+          const float m2 = fmaxf(m[h], mz);
           l[h] *= m[h] == m2 ? 1.f : ex2_ftz(m[h] - m2);
           m[h] = m2;
-          const float grow = mx + lv;
-          float M2 = M[h];
-          if (grow > M2 + P_LAZY) M2 = grow;
+          const float M2 = mw > M[h] + P_LAZY ? mw : M[h];
           al[h] = M2 == M[h] || M[h] == -INFINITY ? 1.f : ex2_ftz(M[h] - M2);
           M[h] = M2;
           // rows without a reference yet have seen nothing: their z are all -inf
           const float Mu = M2 == -INFINITY ? 0.f : M2, mu = m2 == -INFINITY ? 0.f : m2;
-          const float add = lv - Mu + P_OFF;
-          float e[4];
+          float sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; k++) e[k] = ex2_ftz(fmaf(z[h][k], c, add));
-          l[h] = fmaf((e[0] + e[1]) + (e[2] + e[3]), wl * ex2_ftz(Mu - P_OFF - lvref - mu), l[h]);
-          pf[h] = half2_of(e[0], e[1]);
-          pf[2 + h] = half2_of(e[2], e[3]);
-          if (poison) {
-            for (uint32_t b = poison; b; b &= b - 1) {
-              const int j = j0 + __ffs(b) - 1;
-              if (j >= lo_r[h] && j < hi_r[h]) l[h] = NAN;
-            }
+          for (int g = 0; g < NG; g++) {
+            float e[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) e[k] = ex2_ftz(fmaf(z[g][h][k], c[g], lv[g] - Mu + P_OFF));
+            sum = fmaf((e[0] + e[1]) + (e[2] + e[3]), wl[g], sum);
+            pf[g][h] = half2_of(e[0], e[1]);
+            pf[g][2 + h] = half2_of(e[2], e[3]);
+          }
+          l[h] = fmaf(sum, lvref == -INFINITY ? 0.f : ex2_ftz(Mu - P_OFF - lvref - mu), l[h]);
+          for (uint32_t b = poison; b; b &= b - 1) {
+            const int j = j0 + __ffs(b) - 1;
+            if (j >= lo_r[h] && j < hi_r[h]) l[h] = NAN;
           }
         }
         if (__any_sync(~0u, al[0] != 1.f || al[1] != 1.f)) {
@@ -373,21 +404,23 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
         // O += P V: pieces c, c + 1 per ldmatrix
 #pragma unroll
-        for (int c = 0; c < C::PIECES; c += 2) {
-          uint32_t r[4];
-          ldsm4t(vb + piece<D>((lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), r);
+        for (int c = 0; c < C::PIECES; c += 2)
 #pragma unroll
-          for (int u = 0; u < 2; u++) {
-            // bytes (row 2t dim 2n, row 2t dim 2n+1, row 2t+1 dim 2n, row 2t+1 dim 2n+1)
-            const uint32_t x0 = __byte_perm(r[2 * u], 0, 0x3120), x1 = __byte_perm(r[2 * u + 1], 0, 0x3120);
-            float ev[4] = {o[c + u][0], o[c + u][2], o[c + u][4], o[c + u][6]};
-            float od[4] = {o[c + u][1], o[c + u][3], o[c + u][5], o[c + u][7]};
-            mma16816(ev, pf, half2_of_codes(uint16_t(x0)), half2_of_codes(uint16_t(x1)));
-            mma16816(od, pf, half2_of_codes(uint16_t(x0 >> 16)), half2_of_codes(uint16_t(x1 >> 16)));
-            o[c + u][0] = ev[0]; o[c + u][2] = ev[1]; o[c + u][4] = ev[2]; o[c + u][6] = ev[3];
-            o[c + u][1] = od[0]; o[c + u][3] = od[1]; o[c + u][5] = od[2]; o[c + u][7] = od[3];
+          for (int g = 0; g < NG; g++) {
+            uint32_t r[4];
+            ldsm4t(vb + piece<D>(g * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), r);
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+              // bytes (row 2t dim 2n, row 2t dim 2n+1, row 2t+1 dim 2n, row 2t+1 dim 2n+1)
+              const uint32_t x0 = __byte_perm(r[2 * u], 0, 0x3120), x1 = __byte_perm(r[2 * u + 1], 0, 0x3120);
+              float ev[4] = {o[c + u][0], o[c + u][2], o[c + u][4], o[c + u][6]};
+              float od[4] = {o[c + u][1], o[c + u][3], o[c + u][5], o[c + u][7]};
+              mma16816(ev, pf[g], half2_of_codes(uint16_t(x0)), half2_of_codes(uint16_t(x1)));
+              mma16816(od, pf[g], half2_of_codes(uint16_t(x0 >> 16)), half2_of_codes(uint16_t(x1 >> 16)));
+              o[c + u][0] = ev[0]; o[c + u][2] = ev[1]; o[c + u][4] = ev[2]; o[c + u][6] = ev[3];
+              o[c + u][1] = od[0]; o[c + u][3] = od[1]; o[c + u][5] = od[2]; o[c + u][7] = od[3];
+            }
           }
-        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
