@@ -144,7 +144,7 @@ size_t paged_attn_workspace_bytes(int T, int H, int Hkv, int d) {
   using namespace paged;
   if (T < 1 || H < 1 || Hkv < 1) return 0;
   const int G = H / Hkv;
-  return (G <= ROWS_SMALL ? split_workspace(rows_blocks(), ROWS_SMALL, d) : 0) +
+  return (G <= ROWS_SMALL ? split_workspace(std::min(1024, ROWS_BLOCKS_MOST * num_sms()), ROWS_SMALL, d) : 0) +
          ((long long)T * G > ROWS_SMALL ? split_workspace(tile_blocks(), ROWS_ITEM, d) : 0);
 }
 
@@ -162,13 +162,15 @@ hcl_status_t launch_paged_attn(const PagedAttnArgs& a, void* ws, cudaStream_t st
   p.limit = wait_limit_cycles();
   uint8_t* at = static_cast<uint8_t*>(ws);
   if (p.G <= ROWS_SMALL) {
-    p.n_blocks = rows_blocks();
+    // (small requests have up to 8 rows, unless the call's bounds let them have up to 16)
+    const int rows = (int)std::min<long long>(ROWS_SMALL, (long long)std::min(a.max_q, a.T) * p.G);
+    p.n_blocks = rows_blocks(rows, a.kv.d, a.kv.v == nullptr);
     p.meta = reinterpret_cast<Meta*>(at);
     p.part = reinterpret_cast<float*>(at + meta_bytes(p.n_blocks));
-    hcl_status_t e = launch_rows(p, st);
+    hcl_status_t e = launch_rows(p, rows, st);
     if (e == HCL_OK) e = launch_merge(p, ROWS_SMALL, st);
     if (e != HCL_OK) return e;
-    at += split_workspace(p.n_blocks, ROWS_SMALL, a.kv.d);
+    at += split_workspace(std::min(1024, ROWS_BLOCKS_MOST * num_sms()), ROWS_SMALL, a.kv.d);
   }
   if ((long long)std::min(a.max_q, a.T) * p.G <= ROWS_SMALL) return HCL_OK;
   p.n_blocks = tile_blocks();

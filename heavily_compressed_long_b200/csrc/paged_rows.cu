@@ -1,20 +1,22 @@
 // paged_rows.cu -- paged attention for requests with few query rows (queries x heads of one KV
 // head <= 16): decode and short drafts.  One pass over the codes, bound by HBM.
 //
-// Block: one producer warp and four consumer warps, two blocks per SM.  A unit is 64 KV rows of
-// one request and KV head.  The producer copies its codes with TMA (one box per page, or per 64
-// rows of a longer page) into a ring of swizzled stages and its page scales with 4-byte
-// asynchronous copies that complete on the same mbarrier; page ids are read eight units at a time,
-// eight ahead.  Consumer warps 0, 1 take the even units and 2, 3 the odd ones, each 32 rows and
-// its own running softmax, so warps never wait for one another inside an item.  (With 16 rows of
-// every unit to each warp the chain from load to store, not the bytes, set the pace: 300 us for
-// 1.37 GB; with 32, 265 us; 64 gain nothing more.)
-//   S (16 query rows x 32 KV rows) by m16n8k16 fp16 MMAs; the K fragments come from ldmatrix on
+// Block: one producer warp and four consumer warps; two or three blocks per SM.  A unit is 64 KV rows of one request and KV head.  The
+// producer copies its codes with TMA (one box per page, or per 64 rows of a longer page) into a
+// ring of swizzled stages and its page scales with 4-byte asynchronous copies that complete on
+// the same mbarrier; page ids are read eight units at a time, eight ahead.  Consumer warps 0, 1
+// take the even units and 2, 3 the odd ones, each 32 rows and its own running softmax, so warps
+// never wait for one another inside an item:
+//   S^T (16 KV rows x 8 query rows) by m16n8k16 fp16 MMAs: KV rows are the M of the MMA, so up to
+//   8 query rows (a group of 8 heads) waste none of it.  The K fragments come from ldmatrix on
 //   the codes (a 16-byte piece of a row is one k-step, its dimensions taken in the order that
 //   gives each thread four neighbouring codes; Q is laid out alike) and a conversion to fp16;
-//   O += P V the same way from transposed ldmatrix on pairs of codes (even and odd dimensions
-//   make two n-tiles).
-// The tensor cores run at a fraction of their rate here; the bytes bound the kernel.
+//   O^T (16 dimensions x 8 query rows) += V^T P^T from transposed ldmatrix on pairs of codes (a
+//   pair's even and odd dimensions are rows m and m + 8); P^T is S^T's layout transposed
+//   (movmatrix).
+// The bytes bound the kernel once the chain from load to store is covered: with query rows as M,
+// 16 KV rows a warp and step and two blocks, 1.37 GB took 300 us; with 32 KV rows 265 us; this
+// form: see the table of measurements.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -29,17 +31,28 @@ constexpr int TILE = 64;               // KV rows per unit
 constexpr int NG = 2;                  // groups of 16 rows (never more than a page) per warp and unit
 constexpr int WPT = TILE / (16 * NG);  // warps per unit
 
-template <int D, bool SHARED>
+// Blocks per SM: three where the registers (8 query rows) and an even number of stages allow it.
+constexpr int blocks_per_sm(int nt, int d, bool shared) { return nt == 1 && !(d == 128 && !shared) ? 3 : 2; }
+
+// NT: query rows / 8
+template <int D, bool SHARED, int NT>
 struct Cfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int BLOCKS = blocks_per_sm(NT, D, SHARED);
   static constexpr int PLANE = TILE * D;
   static constexpr int STAGE = PLANE * (SHARED ? 1 : 2);
-  static constexpr int STAGES = D == 128 ? (SHARED ? 8 : 4) : 8;
+  static constexpr int RING = BLOCKS == 3 ? 49152 : 65536;
+  static constexpr int STAGES = RING / STAGE < 8 ? RING / STAGE : 8;
+  // A stage always belongs to the same consumer warps: a warp that waited on every other phase of
+  // a barrier could take an old phase for the one it wants.
+  static_assert(STAGES % (NW / WPT) == 0, "stages");
   static constexpr int PIECES = D / 16;  // 16-byte pieces of a row = k-steps
-  static constexpr uint32_t SCALES = STAGES * STAGE;                // [STAGES][2][4] floats
-  static constexpr uint32_t MERGE = SCALES + STAGES * 32;           // [NW - 1][16][D] floats
-  static constexpr uint32_t STATS = MERGE + (NW - 1) * 16 * D * 4;  // [NW][16][3] floats
-  static constexpr uint32_t BAR = STATS + NW * 16 * 3 * 4;
-  static constexpr uint32_t SCRATCH = BAR + 2 * STAGES * 8;         // find_share
+  static constexpr int PITCH = D + 4;    // floats of a row in the exchange
+  static constexpr uint32_t SCALES = STAGES * STAGE;                    // [STAGES][2][4] floats
+  static constexpr uint32_t MERGE = SCALES + STAGES * 32;               // [NW][ROWS][PITCH] floats
+  static constexpr uint32_t STATS = MERGE + NW * ROWS * PITCH * 4;      // [NW][ROWS][3] floats
+  static constexpr uint32_t BAR = STATS + NW * ROWS * 3 * 4;
+  static constexpr uint32_t SCRATCH = BAR + 2 * STAGES * 8;             // find_share
   static constexpr uint32_t MISC = SCRATCH + (NW + 1 + 4) * 8;
   static constexpr uint32_t TOTAL = MISC + 16;
 };
@@ -59,6 +72,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit values held in fragment layout.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // Byte address of 16-byte piece `c` of row `r` in a swizzled plane (128-byte rows: 128B mode,
@@ -115,10 +135,10 @@ __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
   return true;
 }
 
-template <int D, bool SHARED>
-__global__ void __launch_bounds__(THREADS, 2)
+template <int D, bool SHARED, int NT>
+__global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
     paged_rows_kernel(const Params p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-  using C = Cfg<D, SHARED>;
+  using C = Cfg<D, SHARED, NT>;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset: the compiler still sees shared memory)
   float* s_scale = reinterpret_cast<float*>(sm + C::SCALES);
@@ -222,54 +242,74 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 
   // -------------------------------------------------------------------- consumers
-  const int r0 = lane >> 2, t4 = lane & 3;  // fragment row (and + 8), column group
+  // r0: KV row (and + 8) of a score, even / odd dimension pair of an output, query row of a Q
+  // fragment; this thread's query rows: 8 n + 2 t4 + e, n < NT, e < 2
+  const int r0 = lane >> 2, t4 = lane & 3;
+  constexpr int NR = 2 * NT;
   uint32_t it = 0;
   bool ok = true;
   do {
-    // Q rows r0, r0 + 8 (row = query * G + head), dims 16c + 4 t4 .. + 3 of every piece
     const int nrows = w.r.nq * p.G;
-    uint32_t qf[C::PIECES][4];
-    float back[2];
-    int hi_r[2], lo_r[2];
+    // Q rows r0 + 8 n (row = query * G + head), dims 16c + 4 t4 .. + 3 of every piece
+    uint32_t qf[C::PIECES][NT][2];
+    float back[NR];
+    int hi_r[NR], lo_r[NR];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const int row = r0 + 8 * h;
+    for (int n = 0; n < NT; n++) {
+      const int row = r0 + 8 * n;
       const bool valid = row < nrows;
       const int i = valid ? p.by_G.div(row) : 0, head = w.g * p.G + (valid ? row - i * p.G : 0);
-      hi_r[h] = valid ? vis_hi(p, w.r, i) : 0;
-      lo_r[h] = valid ? vis_lo(p, w.r, i) : 0;
       const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.q) +
                                                         (int64_t)(w.r.c0 + i) * p.a.q_stride + head * D) + t4;
       uint2 x[C::PIECES];
       float am = 0.f;
 #pragma unroll
+      for (int c = 0; c < C::PIECES; c++) x[c] = valid ? __ldg(src + c * 4) : make_uint2(0, 0);
+#pragma unroll
       for (int c = 0; c < C::PIECES; c++) {
-        x[c] = valid ? __ldg(src + c * 4) : make_uint2(0, 0);
         const uint32_t a[2] = {x[c].x, x[c].y};
 #pragma unroll
         for (int k = 0; k < 2; k++)
-          am = fmaxf(am, fmaxf(fabsf(__uint_as_float(a[k] << 16)), fabsf(__uint_as_float(a[k] & 0xFFFF0000u))));
+          am = fmax3(am, fabsf(__uint_as_float(a[k] << 16)), fabsf(__uint_as_float(a[k] & 0xFFFF0000u)));
       }
       am = fmaxf(am, __shfl_xor_sync(~0u, am, 1));
       am = fmaxf(am, __shfl_xor_sync(~0u, am, 2));
-      const float f = row_factor(am, &back[h]);
+      float bk;
+      const float f = row_factor(am, &bk);
+#pragma unroll
+      for (int e = 0; e < 2; e++) back[2 * n + e] = __shfl_sync(~0u, bk, (2 * t4 + e) * 4);
 #pragma unroll
       for (int c = 0; c < C::PIECES; c++) {
-        qf[c][h] = half2_of(__uint_as_float(x[c].x << 16) * f, __uint_as_float(x[c].x & 0xFFFF0000u) * f);
-        qf[c][2 + h] = half2_of(__uint_as_float(x[c].y << 16) * f, __uint_as_float(x[c].y & 0xFFFF0000u) * f);
+        qf[c][n][0] = half2_of(__uint_as_float(x[c].x << 16) * f, __uint_as_float(x[c].x & 0xFFFF0000u) * f);
+        qf[c][n][1] = half2_of(__uint_as_float(x[c].y << 16) * f, __uint_as_float(x[c].y & 0xFFFF0000u) * f);
       }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; r++) {
+      const int row = 8 * (r >> 1) + 2 * t4 + (r & 1);
+      const bool valid = row < nrows;
+      const int i = valid ? p.by_G.div(row) : 0;
+      hi_r[r] = valid ? vis_hi(p, w.r, i) : 0;
+      lo_r[r] = valid ? vis_lo(p, w.r, i) : 0;
     }
     // the rows that all queries see, and that any sees
     const int all_lo = vis_lo(p, w.r, w.r.nq - 1), all_hi = vis_hi(p, w.r, 0);
     const int any_lo = vis_lo(p, w.r, 0), any_hi = vis_hi(p, w.r, w.r.nq - 1);
 
-    float o[C::PIECES][8];  // [piece][row half][dims 4 t4 .. + 3]
+    float o[C::PIECES][NT][4];  // dims 16 c + 2 r0 (+ 1 for the last two), query rows of n (e = k & 1)
 #pragma unroll
     for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
-      for (int k = 0; k < 8; k++) o[c][k] = 0.f;
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int k = 0; k < 4; k++) o[c][n][k] = 0.f;
     const int rows0 = (warp % WPT) * 16 * NG;  // this warp's rows of a tile
-    float m[2] = {-INFINITY, -INFINITY}, M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lvref = -INFINITY;
+    float m[NR], M[NR], l[NR], lvref = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < NR; r++) {
+      m[r] = M[r] = -INFINITY;
+      l[r] = 0.f;
+    }
 
     for (int i = 0; i < w.count; i++, it++) {
       if (it % (NW / WPT) != warp / WPT) continue;
@@ -284,42 +324,42 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (j0 < any_hi && j0 + 16 * NG > any_lo) {
         const uint32_t kb = smem_u32(sm + st * C::STAGE) + rows0 * D;
         const uint32_t vb = kb + (SHARED ? 0 : C::PLANE);
-        // S
-        float s[2 * NG][4];  // [n-tile]
-#pragma unroll
-        for (int n = 0; n < 2 * NG; n++)
-#pragma unroll
-          for (int k = 0; k < 4; k++) s[n][k] = 0.f;
-#pragma unroll
-        for (int q = 0; q < C::PIECES / 4; q++)
-#pragma unroll
-          for (int n = 0; n < 2 * NG; n++) {
-            uint32_t r[4];
-            ldsm4(kb + piece<D>(n * 8 + (lane & 7), q * 4 + (lane >> 3)), r);
-#pragma unroll
-            for (int c = 0; c < 4; c++)
-              mma16816(s[n], qf[q * 4 + c], half2_of_codes(uint16_t(r[c])), half2_of_codes(uint16_t(r[c] >> 16)));
-          }
-        float z[NG][2][4];  // [group][row half][columns 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4]
+        // rows (lane & 15) of a group, piece (lane >> 4) of two
+        const int frow = lane & 15, fpiece = lane >> 4;
+        // S^T: z[g][n][k]: KV row 16 g + r0 + 8 (k >> 1), query row 8 n + 2 t4 + (k & 1)
+        float z[NG][NT][4];
 #pragma unroll
         for (int g = 0; g < NG; g++)
 #pragma unroll
-          for (int h = 0; h < 2; h++)
+          for (int n = 0; n < NT; n++)
 #pragma unroll
-            for (int k = 0; k < 4; k++)  // (a group without a page is left out)
-              z[g][h][k] = ks[g] > 0.f ? s[2 * g + (k >> 1)][2 * h + (k & 1)] : -INFINITY;
+            for (int k = 0; k < 4; k++) z[g][n][k] = 0.f;
+#pragma unroll
+        for (int c = 0; c < C::PIECES; c += 2)
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            uint32_t r[4];
+            ldsm4(kb + piece<D>(g * 16 + frow, c + fpiece), r);
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+              const uint32_t a[4] = {half2_of_codes(uint16_t(r[2 * u])), half2_of_codes(uint16_t(r[2 * u + 1])),
+                                     half2_of_codes(uint16_t(r[2 * u] >> 16)), half2_of_codes(uint16_t(r[2 * u + 1] >> 16))};
+#pragma unroll
+              for (int n = 0; n < NT; n++) mma16816(z[g][n], a, qf[c + u][n][0], qf[c + u][n][1]);
+            }
+          }
         uint32_t poison = 0;  // a bit for each of the KV rows
         static_assert(16 * NG <= 32, "poison");
         if (j0 < all_lo || j0 + 16 * NG > all_hi || !(ks[0] > 0.f) || !(ks[NG - 1] > 0.f)) {
-          // some row does not see some of these KV rows
+          // some query row does not see some of these KV rows, or a group has no page
 #pragma unroll
           for (int g = 0; g < NG; g++)
 #pragma unroll
-            for (int h = 0; h < 2; h++)
+            for (int n = 0; n < NT; n++)
 #pragma unroll
               for (int k = 0; k < 4; k++) {
-                const int j = j0 + g * 16 + (k >> 1) * 8 + 2 * t4 + (k & 1);
-                if (j < lo_r[h] || j >= hi_r[h]) z[g][h][k] = -INFINITY;
+                const int j = j0 + g * 16 + r0 + 8 * (k >> 1), r = 2 * n + (k & 1);
+                if (j < lo_r[r] || j >= hi_r[r] || !(ks[g] > 0.f)) z[g][n][k] = -INFINITY;
               }
           // NaN codes among the values would reach the rows that do not see them (0 * NaN), and
           // rows behind the last (or of no page) hold anything: they become 0, and `poison` says
@@ -329,8 +369,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
           for (int g = 0; g < NG; g++)
 #pragma unroll
-            for (int i = 0; i < C::PIECES / 2; i++) {
-              const int e = i * 32 + lane;  // piece of the group
+            for (int i2 = 0; i2 < C::PIECES / 2; i2++) {
+              const int e = i2 * 32 + lane;  // piece of the group
               uint4* at = reinterpret_cast<uint4*>(vp + g * 16 * D + e * 16);
               const uint4 v = *at;
               const uint4 n4 = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
@@ -355,70 +395,76 @@ __global__ void __launch_bounds__(THREADS, 2)
           lv[g] = ks[g] > 0.f ? fmaxf(lv[g], lvref - LV_SPAN) : lvref;
           wl[g] = ks[g] > 0.f ? ex2_ftz(lvref - lv[g]) : 0.f;
         }
-        float al[2];
-        uint32_t pf[NG][4];
+        float al[NR], e[NG][NR][2];
+        bool grew = false;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
+        for (int r = 0; r < NR; r++) {
+          const int n = r >> 1, q = r & 1;
           float c[NG], mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
 #pragma unroll
           for (int g = 0; g < NG; g++) {
-            c[g] = fmaxf(kc[g] * back[h], SCALE_MIN);
-            const float x = fmax3(fmaxf(z[g][h][0], z[g][h][1]), z[g][h][2], z[g][h][3]) * c[g];
+            c[g] = fmaxf(kc[g] * back[r], SCALE_MIN);
+            const float x = fmaxf(z[g][n][q], z[g][n][2 + q]) * c[g];
             mz = fmaxf(mz, x);
             mw = fmaxf(mw, x + lv[g]);
           }
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            mz = fmaxf(mz, __shfl_xor_sync(~0u, mz, o));
-            mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, o));
+          for (int o2 = 4; o2 < 32; o2 <<= 1) {
+            mz = fmaxf(mz, __shfl_xor_sync(~0u, mz, o2));
+            mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, o2));
           }
-          const float m2 = fmaxf(m[h], mz);
-          l[h] *= m[h] == m2 ? 1.f : ex2_ftz(m[h] - m2);
-          m[h] = m2;
-          const float M2 = mw > M[h] + P_LAZY ? mw : M[h];
-          al[h] = M2 == M[h] || M[h] == -INFINITY ? 1.f : ex2_ftz(M[h] - M2);
-          M[h] = M2;
+          const float m2 = fmaxf(m[r], mz);
+          l[r] *= m[r] == m2 ? 1.f : ex2_ftz(m[r] - m2);
+          m[r] = m2;
+          const float M2 = mw > M[r] + P_LAZY ? mw : M[r];
+          al[r] = M2 == M[r] || M[r] == -INFINITY ? 1.f : ex2_ftz(M[r] - M2);
+          grew |= al[r] != 1.f;
+          M[r] = M2;
           // rows without a reference yet have seen nothing: their z are all -inf
           const float Mu = M2 == -INFINITY ? 0.f : M2, mu = m2 == -INFINITY ? 0.f : m2;
           float sum = 0.f;
 #pragma unroll
           for (int g = 0; g < NG; g++) {
-            float e[4];
 #pragma unroll
-            for (int k = 0; k < 4; k++) e[k] = ex2_ftz(fmaf(z[g][h][k], c[g], lv[g] - Mu + P_OFF));
-            sum = fmaf((e[0] + e[1]) + (e[2] + e[3]), wl[g], sum);
-            pf[g][h] = half2_of(e[0], e[1]);
-            pf[g][2 + h] = half2_of(e[2], e[3]);
+            for (int k = 0; k < 2; k++) e[g][r][k] = ex2_ftz(fmaf(z[g][n][2 * k + q], c[g], lv[g] - Mu + P_OFF));
+            sum = fmaf(e[g][r][0] + e[g][r][1], wl[g], sum);
           }
-          l[h] = fmaf(sum, lvref == -INFINITY ? 0.f : ex2_ftz(Mu - P_OFF - lvref - mu), l[h]);
+          l[r] = fmaf(sum, lvref == -INFINITY ? 0.f : ex2_ftz(Mu - P_OFF - lvref - mu), l[r]);
           for (uint32_t b = poison; b; b &= b - 1) {
             const int j = j0 + __ffs(b) - 1;
-            if (j >= lo_r[h] && j < hi_r[h]) l[h] = NAN;
+            if (j >= lo_r[r] && j < hi_r[r]) l[r] = NAN;
           }
         }
-        if (__any_sync(~0u, al[0] != 1.f || al[1] != 1.f)) {
+        uint32_t pb[NG][NT][2];  // P^T fragments
+#pragma unroll
+        for (int g = 0; g < NG; g++)
+#pragma unroll
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int k = 0; k < 2; k++) pb[g][n][k] = transpose8(half2_of(e[g][2 * n][k], e[g][2 * n + 1][k]));
+        if (__any_sync(~0u, grew)) {
 #pragma unroll
           for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
-            for (int k = 0; k < 8; k++) o[c][k] *= al[k >> 2];
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+              for (int k = 0; k < 4; k++) o[c][n][k] *= al[2 * n + (k & 1)];
         }
-        // O += P V: pieces c, c + 1 per ldmatrix
+        // O^T += V^T P^T: pieces c, c + 1 per ldmatrix
 #pragma unroll
         for (int c = 0; c < C::PIECES; c += 2)
 #pragma unroll
           for (int g = 0; g < NG; g++) {
             uint32_t r[4];
-            ldsm4t(vb + piece<D>(g * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), r);
+            ldsm4t(vb + piece<D>(g * 16 + frow, c + fpiece), r);
 #pragma unroll
             for (int u = 0; u < 2; u++) {
               // bytes (row 2t dim 2n, row 2t dim 2n+1, row 2t+1 dim 2n, row 2t+1 dim 2n+1)
               const uint32_t x0 = __byte_perm(r[2 * u], 0, 0x3120), x1 = __byte_perm(r[2 * u + 1], 0, 0x3120);
-              float ev[4] = {o[c + u][0], o[c + u][2], o[c + u][4], o[c + u][6]};
-              float od[4] = {o[c + u][1], o[c + u][3], o[c + u][5], o[c + u][7]};
-              mma16816(ev, pf[g], half2_of_codes(uint16_t(x0)), half2_of_codes(uint16_t(x1)));
-              mma16816(od, pf[g], half2_of_codes(uint16_t(x0 >> 16)), half2_of_codes(uint16_t(x1 >> 16)));
-              o[c + u][0] = ev[0]; o[c + u][2] = ev[1]; o[c + u][4] = ev[2]; o[c + u][6] = ev[3];
-              o[c + u][1] = od[0]; o[c + u][3] = od[1]; o[c + u][5] = od[2]; o[c + u][7] = od[3];
+              const uint32_t a[4] = {half2_of_codes(uint16_t(x0)), half2_of_codes(uint16_t(x0 >> 16)),
+                                     half2_of_codes(uint16_t(x1)), half2_of_codes(uint16_t(x1 >> 16))};
+#pragma unroll
+              for (int n = 0; n < NT; n++) mma16816(o[c + u][n], a, pb[g][n][0], pb[g][n][1]);
             }
           }
       }
@@ -429,49 +475,23 @@ __global__ void __launch_bounds__(THREADS, 2)
       *s_abort = 1;
       if (lane == 0) report(p.a.status, HCL_ERR_TIMEOUT);
     }
-    // join the warps: l's partial sums lie over the four threads of a row
+    // join the warps: l's partial sums lie over the eight threads of a query row
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      l[h] += __shfl_xor_sync(~0u, l[h], 1);
-      l[h] += __shfl_xor_sync(~0u, l[h], 2);
-      if (t4 == 0) {
-        float* s3 = s_stat + (warp * 16 + r0 + 8 * h) * 3;
-        s3[0] = m[h]; s3[1] = M[h]; s3[2] = l[h];
+    for (int r = 0; r < NR; r++) {
+#pragma unroll
+      for (int o2 = 4; o2 < 32; o2 <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], o2);
+      if (r0 == 0) {
+        float* s3 = s_stat + (warp * C::ROWS + 8 * (r >> 1) + 2 * t4 + (r & 1)) * 3;
+        s3[0] = m[r]; s3[1] = M[r]; s3[2] = l[r];
       }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
-    float mt[2], Mt[2], lt[2];
+    // O in its own reference; the readers weigh it
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      mt[h] = Mt[h] = -INFINITY;
-      lt[h] = 0.f;
+    for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
-      for (int v = 0; v < NW; v++) {
-        const float* s3 = s_stat + (v * 16 + r0 + 8 * h) * 3;
-        mt[h] = fmaxf(mt[h], s3[0]);
-        Mt[h] = fmaxf(Mt[h], s3[1]);
-      }
-#pragma unroll
-      for (int v = 0; v < NW; v++) {
-        const float* s3 = s_stat + (v * 16 + r0 + 8 * h) * 3;
-        lt[h] += s3[0] == -INFINITY ? s3[2] : s3[2] * ex2_ftz(s3[0] - mt[h]);
-      }
-      const float f = M[h] == -INFINITY ? 0.f : ex2_ftz(M[h] - Mt[h]);
-      if (f != 1.f) {
-#pragma unroll
-        for (int c = 0; c < C::PIECES; c++)
-#pragma unroll
-          for (int k = 0; k < 4; k++) o[c][4 * h + k] = f == 0.f ? 0.f : o[c][4 * h + k] * f;
-      }
-    }
-    if (warp > 0) {
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-#pragma unroll
-        for (int c = 0; c < C::PIECES; c++)
-          *reinterpret_cast<float4*>(s_merge + ((warp - 1) * 16 + r0 + 8 * h) * D + ((c ^ (r0 & 7)) & (C::PIECES - 1)) * 16 + t4 * 4) =
-              make_float4(o[c][4 * h], o[c][4 * h + 1], o[c][4 * h + 2], o[c][4 * h + 3]);
-    }
+      for (int r = 0; r < NR; r++)
+        *reinterpret_cast<float2*>(s_merge + (warp * C::ROWS + 8 * (r >> 1) + 2 * t4 + (r & 1)) * C::PITCH + c * 16 + 2 * r0) =
+            make_float2(o[c][r >> 1][r & 1], o[c][r >> 1][2 + (r & 1)]);
     // (a warp whose wait ran out ends the block here, at the same item for all four)
     uint32_t gone;
     asm volatile(
@@ -479,46 +499,54 @@ __global__ void __launch_bounds__(THREADS, 2)
         "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(gone) : "r"(uint32_t(!ok)), "n"(NW * 32) : "memory");
     if (gone) break;
-    if (warp == 0) {
+    {
+      // all four warps: rows of D / 4 threads with four dimensions each
       const bool whole = w.count == w.nt;
+      float* pp = p.part + (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * part_floats(ROWS_SMALL, D);
+      constexpr int TPR = D / 4;
+      const int col = (tid % TPR) * 4;
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int row = r0 + 8 * h;
-        const bool valid = row < nrows;
-        const int i = valid ? p.by_G.div(row) : 0, head = w.g * p.G + (valid ? row - i * p.G : 0);
-        const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
-        float f = 1.f, lse = 0.f;
-        float* pp = p.part + (2 * (size_t)blockIdx.x + (w.tile == 0 ? 1 : 0)) * part_floats(ROWS_SMALL, D);
+      for (int k = 0; k < C::ROWS * TPR / (NW * 32); k++) {
+        const int row = tid / TPR + k * (NW * 32 / TPR);
+        float mt = -INFINITY, Mt = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int v = 0; v < NW; v++) {
+          const float* s3 = s_stat + (v * C::ROWS + row) * 3;
+          mt = fmaxf(mt, s3[0]);
+          Mt = fmaxf(Mt, s3[1]);
+        }
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < NW; v++) {
+          const float* s3 = s_stat + (v * C::ROWS + row) * 3;
+          lt += s3[0] == -INFINITY ? s3[2] : s3[2] * ex2_ftz(s3[0] - mt);
+          const float f = s3[1] == -INFINITY ? 0.f : ex2_ftz(s3[1] - Mt);
+          if (f != 0.f) {
+            const float4 x = *reinterpret_cast<const float4*>(s_merge + (v * C::ROWS + row) * C::PITCH + col);
+            a.x = fmaf(x.x, f, a.x); a.y = fmaf(x.y, f, a.y); a.z = fmaf(x.z, f, a.z); a.w = fmaf(x.w, f, a.w);
+          }
+        }
+        if (row >= nrows) continue;
         if (whole) {
-          const float sink2 = p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY;
-          f = finish_row(mt[h], Mt[h], lt[h], sink2, &lse);
-        } else if (t4 == 0) {
-          *reinterpret_cast<float4*>(pp + row * 4) = make_float4(mt[h], Mt[h], lt[h], 0.f);
+          const int i = p.by_G.div(row), head = w.g * p.G + row - i * p.G;
+          const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
+          float lse;
+          const float f = finish_row(mt, Mt, lt, p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + col) =
+              f == 0.f ? make_uint2(0, 0) : make_uint2(bf16x2_of(a.x * f, a.y * f), bf16x2_of(a.z * f, a.w * f));
+          if (col == 0 && p.a.lse) p.a.lse[orow] = lse;
+        } else {
+          *reinterpret_cast<float4*>(pp + ROWS_SMALL * 4 + row * D + col) = a;
+          if (col == 0) *reinterpret_cast<float4*>(pp + row * 4) = make_float4(mt, Mt, lt, 0.f);
         }
-#pragma unroll
-        for (int c = 0; c < C::PIECES; c++) {
-          float4 a = make_float4(o[c][4 * h], o[c][4 * h + 1], o[c][4 * h + 2], o[c][4 * h + 3]);
-#pragma unroll
-          for (int v = 0; v < NW - 1; v++) {
-            const float4 x = *reinterpret_cast<const float4*>(s_merge + (v * 16 + row) * D + ((c ^ (r0 & 7)) & (C::PIECES - 1)) * 16 + t4 * 4);
-            a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-          }
-          if (whole) {
-            if (valid)
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + c * 16 + t4 * 4) =
-                  f == 0.f ? make_uint2(0, 0)
-                           : make_uint2(bf16x2_of(a.x * f, a.y * f), bf16x2_of(a.z * f, a.w * f));
-          } else {
-            *reinterpret_cast<float4*>(pp + 64 + row * D + c * 16 + t4 * 4) = a;
-          }
-        }
-        if (whole && valid && t4 == 0 && p.a.lse) p.a.lse[orow] = lse;
       }
     }
+    // the exchange is free again
+    asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
   } while (walk_next(p, w));
 }
 
-template <int D, bool SHARED>
+template <int D, bool SHARED, int NT>
 hcl_status_t launch_t(const Params& p, cudaStream_t st) {
   CUtensorMap tk, tv;
   const int box = std::min(p.a.kv.page, TILE);
@@ -529,9 +557,10 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
     e = code_map(&tv, p.a.kv.v, p.a.kv, box, true);
     if (e != HCL_OK) return e;
   }
-  auto kern = paged_rows_kernel<D, SHARED>;
-  const int smem = (int)Cfg<D, SHARED>::TOTAL + 1024;
-  static_assert(2 * (Cfg<D, SHARED>::TOTAL + 2048) <= 233472, "two blocks per SM");
+  using C = Cfg<D, SHARED, NT>;
+  auto kern = paged_rows_kernel<D, SHARED, NT>;
+  const int smem = (int)C::TOTAL + 1024;
+  static_assert(C::BLOCKS * (C::TOTAL + 2048) <= 233472, "blocks per SM");
   e = set_kernel_attrs(reinterpret_cast<const void*>(kern), smem, false);
   if (e != HCL_OK) return e;
   return check_cuda(launch_pdl(kern, dim3(p.n_blocks), dim3(THREADS), (size_t)smem, st, 1, p, tk, tv),
@@ -540,11 +569,18 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
 
 }  // namespace
 
-int rows_blocks() { return std::min(1024, 2 * num_sms()); }
+int rows_blocks(int rows, int d, bool shared) {
+  return std::min(1024, blocks_per_sm(rows <= 8 ? 1 : 2, d, shared) * num_sms());
+}
 
-hcl_status_t launch_rows(const Params& p, cudaStream_t st) {
-  if (p.a.kv.d == 128) return p.a.kv.v ? launch_t<128, false>(p, st) : launch_t<128, true>(p, st);
-  return p.a.kv.v ? launch_t<64, false>(p, st) : launch_t<64, true>(p, st);
+hcl_status_t launch_rows(const Params& p, int rows, cudaStream_t st) {
+  const bool d128 = p.a.kv.d == 128, v = p.a.kv.v != nullptr;
+  if (rows <= 8) {
+    if (d128) return v ? launch_t<128, false, 1>(p, st) : launch_t<128, true, 1>(p, st);
+    return v ? launch_t<64, false, 1>(p, st) : launch_t<64, true, 1>(p, st);
+  }
+  if (d128) return v ? launch_t<128, false, 2>(p, st) : launch_t<128, true, 2>(p, st);
+  return v ? launch_t<64, false, 2>(p, st) : launch_t<64, true, 2>(p, st);
 }
 
 hcl_status_t code_map(CUtensorMap* m, const void* codes, const hcl_paged_kv_t& kv, int rows, bool swizzle) {

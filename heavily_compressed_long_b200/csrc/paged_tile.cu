@@ -193,7 +193,7 @@ struct Cfg {
   static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
   static constexpr uint32_t ITEMS = STAT + 128 * 16;
   static constexpr uint32_t BAR = ITEMS + IRING * sizeof(Item);
-  static constexpr int NBAR = 2 * NK + 2 * NV + 4 + 4 + 2 + 2 + 1 + 2 * IRING + 2 * NU;
+  static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 4 + 2 + 1 + 2 * IRING + 2 * NU;
   static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
   static constexpr uint32_t MISC = SCRATCH + (16 + 4) * 8;
   static constexpr uint32_t TOTAL = MISC + 16;
@@ -207,16 +207,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset: the compiler still sees shared memory)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   RoundPar* par = reinterpret_cast<RoundPar*>(sm + C::PAR);
+  // A wait names a phase by its parity, so every waiter of a barrier follows it phase by phase, or
+  // knows by other means that the phase before the wanted one has completed and the one after it
+  // cannot: hence a barrier for each buffer.
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + C::BAR);
   uint64_t* k_empty = k_full + C::NK;
   uint64_t* v_full = k_empty + C::NK;
   uint64_t* v_empty = v_full + C::NV;
   uint64_t* s_full = v_empty + C::NV;        // [tile][buffer] S of a step in TMEM
   uint64_t* p_full = s_full + 4;             // [tile][buffer] P in TMEM, O rescaled
-  uint64_t* o_done = s_full + 8;             // [tile] PV of the step completed
-  uint64_t* q_full = s_full + 10;            // [tile] Q tile in shared memory
-  uint64_t* drain = s_full + 12;
-  uint64_t* i_full = s_full + 13;            // [IRING] an item's description stands
+  uint64_t* o_done = s_full + 8;             // [tile][buffer] PV of a step completed
+  uint64_t* q_full = s_full + 12;            // [tile] Q tile in shared memory
+  uint64_t* drain = s_full + 14;
+  uint64_t* i_full = s_full + 15;            // [IRING] an item's description stands
   uint64_t* i_empty = i_full + IRING;        // [IRING] every role is done with it
   uint64_t* u_full = i_empty + IRING;        // [NU] a staging unit's codes landed, its round's parameters stand
   uint64_t* u_empty = u_full + C::NU;        // [NU] the widening warps have read it
@@ -226,9 +229,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NK; i++) { mbar_init(&k_full[i], 128); mbar_init(&k_empty[i], 2); }
     for (int i = 0; i < C::NV; i++) { mbar_init(&v_full[i], 128); mbar_init(&v_empty[i], 2); }
-    for (int i = 0; i < 4; i++) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 128); }
+    for (int i = 0; i < 4; i++) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 128); mbar_init(&o_done[i], 1); }
     for (int t = 0; t < 2; t++) {
-      mbar_init(&o_done[t], 1);
       mbar_init(&q_full[t], 128);
     }
     mbar_init(drain, 2);
@@ -415,14 +417,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         // this tile's step k is round k (pair) or 2k + t (single)
         const int steps = pair ? count : (count + 1 - t) / 2;
         const uint32_t aq = pair && t ? dq + (C::QT >> 4) : dq, stride = pair ? 1 : 2;
-        wait(&q_full[pair ? t : 0], qp);
-        qp ^= 1;  // (group 1 arrives on q_full[1] in single mode too)
+        // both, in every item: a barrier whose last phase was not waited for could still be in it,
+        // and show the one before, of the wanted parity (group 1 arrives in single mode too)
+        wait(&q_full[0], qp);
+        wait(&q_full[1], qp);
+        qp ^= 1;
         uint32_t R = rg + (pair ? 0 : t);
         if (steps > 0) issue_s(R, n, aq, !pair);
         for (int k = 0; k < steps && ok; k++, R += stride, n++) {
           // the next step's scores go where P of the last step was: its PV must have completed
           if (k + 1 < steps) {
-            if (k > 0) wait(&o_done[t], (n & 1) ^ 1);
+            if (k > 0) wait(&o_done[2 * t + ((n & 1) ^ 1)], ((n - 1) >> 1) & 1);
             issue_s(R + stride, n + 1, aq, !pair);
           }
           const uint32_t vb = R % C::NV;
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < TILE / 16; ks++)
             umma_ts(tb + O_COL, a0 + ks * 8, b0 + ks * (2048 >> 4), idPV, ks > 0 || k > 0 ? 1u : 0u, lead);
-          commit_lead(&o_done[t], lead);
+          commit_lead(&o_done[2 * t + (n & 1)], lead);
           release(&v_empty[vb], !pair);
         }
         rg += count;
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // rescale O, once PV of the last step is done with it (rows without a reference yet are
           // in their first step or have an O of zeros)
           if (k > 0) {
-            ok = mbar_wait(&o_done[t], (n & 1) ^ 1, p.limit, s_abort);
+            ok = mbar_wait(&o_done[2 * t + ((n & 1) ^ 1)], ((n - 1) >> 1) & 1, p.limit, s_abort);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
           }
@@ -756,7 +761,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_arrive(&p_full[2 * t + (n & 1)]);
       }
       if (ok && steps > 0) {
-        ok = mbar_wait(&o_done[t], (step + steps - 1) & 1, p.limit, s_abort);
+        const uint32_t n = step + steps - 1;
+        ok = mbar_wait(&o_done[2 * t + (n & 1)], (n >> 1) & 1, p.limit, s_abort);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
         for (int k = max(0, steps - 2); ok && k < steps; k++) {

@@ -589,3 +589,31 @@ def test_binding_refusals(hcl):
     # nothing to do
     hcl.hcl_paged_write(x[:0], None, i32([]), store)
     hcl.hcl_paged_attn(q[:0], i32([0, 0]), i32([0]), store, i32([[0, 1]]), i32([3]), out[:0])
+
+
+@pytest.mark.parametrize("Hkv,G,d,shared,W", [(8, 8, 128, False, 0), (8, 4, 128, True, 0), (4, 16, 128, False, 0),
+                                              (8, 8, 64, False, 0), (4, 16, 64, True, 0), (2, 128, 128, True, 0),
+                                              (4, 64, 64, False, 0), (8, 2, 128, False, 3000)])
+def test_attn_long_rings(hcl, Hkv, G, d, shared, W):
+    """Blocks that run through their rings many times and over several requests and heads: sampled
+    rows against 64 bits."""
+    gen = torch.Generator().manual_seed(11)
+    lens = [70000, 1, 33333, 9000, 64, 50001]
+    page, H, B = 64, Hkv * G, len(lens)
+    table, k, ks, v, vs = make_cache(lens, page, Hkv, d, shared, gen)
+    q = torch.randn(B, H, d, generator=gen).to(torch.bfloat16)
+    dev = lambda t: None if t is None else t.cuda()  # noqa: E731
+    out, lse, st = torch.empty(B, H, d, dtype=torch.bfloat16, device=DEV), torch.empty(B, H, device=DEV), status()
+    scale = 1 / math.sqrt(d)
+    hcl.hcl_paged_attn(q.cuda(), i32(range(B + 1)), i32([n - 1 for n in lens]),
+                       hcl.PagedKV(dev(k), dev(ks), dev(v), dev(vs)), i32(table), i32(lens), out, lse=lse, max_q=1,
+                       W=W, status=st)
+    assert st.item() == 0
+    for b in range(B):
+        for h in (0, G - 1, H // 2, H - 1):
+            g = h // G
+            args = (ref.f64(q[b:b + 1, h:h + 1]), [0, 1], [lens[b] - 1], lens[b:b + 1], table[b:b + 1],
+                    k[:, g:g + 1].numpy(), ks[:, g:g + 1].numpy(), None if shared else v[:, g:g + 1].numpy(),
+                    None if shared else vs[:, g:g + 1].numpy(), page, 1, W, scale)
+            w, wl, mass, zabs = ref.attn(*args)
+            assert_attn(ref.f64(out[b:b + 1, h:h + 1]), ref.f64(lse[b:b + 1, h:h + 1]), w, wl, mass, zabs)
