@@ -14,11 +14,13 @@
 // exact and summed in fp32:  z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
 // A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + 4) with
 // lv = log2(v_scale) and M >= max(z2 + lv) - 11 a running reference, rounded to fp16 (11 bits
-// down to 2^-18 of the largest, nothing below 2^-29), and O = sum P * code in fp32 needs no further scale.  The
-// softmax sum has its own reference m = max z2 (l = sum 2^(z2 - m)), formed from the unrounded P
-// of each group of 16 rows (never more than one page) times 2^(M - 4 - lv - m).  lv is not taken
-// below the largest lv met so far minus 60 (a page of zeros has the scale 2^-126), which keeps
-// every factor in range; its values then count as less than 2^-60 of the largest page's.
+// down to 2^-18 of the largest, nothing below 2^-29), and O = sum P * code in fp32 needs no further scale.
+// The softmax sum is l = sum 2^(z2 - m) with m = M - 4 - lvref, lvref the largest lv met so far:
+// formed from the unrounded P of each group of 16 rows (never more than one page) times
+// 2^(lvref - lv), and moved when M or lvref grow.  Since M <= max z2 + lvref its largest term is
+// not far below 1.  lv is not taken below lvref - 60 (a page of zeros has the scale 2^-126), and
+// where lvref grows so far that l would pass 2^60, M is raised with it: the values of a page
+// whose scale is below 2^-60 of the largest count as zero, its rows' share of the sum does not.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -196,6 +198,16 @@ __device__ __forceinline__ float row_factor(float amax, float* back) {
   const int e = min(max(ex - 127 - 14, -126), 113);  // 2^e
   *back = __uint_as_float(uint32_t(e + 127) << 23);
   return __uint_as_float(uint32_t(127 - e) << 23);
+}
+
+// lvref grows by d: a row's sum moves to the new reference, and its M too where the sum would
+// pass 2^60.
+__device__ __forceinline__ void grow_lvref(float d, float& l, float& M) {
+  if (!(l > 0.f) || M == -INFINITY) return;
+  const float lg = float(int(__float_as_uint(l) >> 23) - 126);  // l < 2^lg
+  const float add = fmaxf(0.f, lg + d - 60.f);
+  l *= exp2f(d - add);
+  M += add;
 }
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {

@@ -304,10 +304,10 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
 #pragma unroll
         for (int k = 0; k < 4; k++) o[c][n][k] = 0.f;
     const int rows0 = (warp % WPT) * 16 * NG;  // this warp's rows of a tile
-    float m[NR], M[NR], l[NR], lvref = -INFINITY;
+    float M[NR], l[NR], lvref = -INFINITY;
 #pragma unroll
     for (int r = 0; r < NR; r++) {
-      m[r] = M[r] = -INFINITY;
+      M[r] = -INFINITY;
       l[r] = 0.f;
     }
 
@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
           __syncwarp();
         }
         float lv[NG], wl[NG], kc[NG];
+        const float lvold = lvref;
 #pragma unroll
         for (int g = 0; g < NG; g++) {
           lv[g] = log2_scale(SHARED ? ks[g] : s_scale[st * 8 + 4 + (rows0 >> 4) + g]);
@@ -395,33 +396,41 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
           lv[g] = ks[g] > 0.f ? fmaxf(lv[g], lvref - LV_SPAN) : lvref;
           wl[g] = ks[g] > 0.f ? ex2_ftz(lvref - lv[g]) : 0.f;
         }
+        float Mo[NR];  // O's reference
+#pragma unroll
+        for (int r = 0; r < NR; r++) Mo[r] = M[r];
+        if (lvref != lvold && lvold != -INFINITY) {  // (the same in all lanes)
+          // (l lies over the eight lanes of a row: their M must move alike)
+#pragma unroll
+          for (int r = 0; r < NR; r++) {
+            float big = l[r];
+#pragma unroll
+            for (int o2 = 4; o2 < 32; o2 <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o2));
+            const float was = M[r];
+            grow_lvref(lvref - lvold, big, M[r]);
+            if (was != -INFINITY) l[r] *= exp2f(lvref - lvold - (M[r] - was));
+          }
+        }
         float al[NR], e[NG][NR][2];
         bool grew = false;
 #pragma unroll
         for (int r = 0; r < NR; r++) {
           const int n = r >> 1, q = r & 1;
-          float c[NG], mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
+          float c[NG], mw = -INFINITY;  // largest z2 + lv
 #pragma unroll
           for (int g = 0; g < NG; g++) {
             c[g] = fmaxf(kc[g] * back[r], SCALE_MIN);
-            const float x = fmaxf(z[g][n][q], z[g][n][2 + q]) * c[g];
-            mz = fmaxf(mz, x);
-            mw = fmaxf(mw, x + lv[g]);
+            mw = fmaxf(mw, fmaf(fmaxf(z[g][n][q], z[g][n][2 + q]), c[g], lv[g]));
           }
 #pragma unroll
-          for (int o2 = 4; o2 < 32; o2 <<= 1) {
-            mz = fmaxf(mz, __shfl_xor_sync(~0u, mz, o2));
-            mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, o2));
-          }
-          const float m2 = fmaxf(m[r], mz);
-          l[r] *= m[r] == m2 ? 1.f : ex2_ftz(m[r] - m2);
-          m[r] = m2;
+          for (int o2 = 4; o2 < 32; o2 <<= 1) mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, o2));
           const float M2 = mw > M[r] + P_LAZY ? mw : M[r];
-          al[r] = M2 == M[r] || M[r] == -INFINITY ? 1.f : ex2_ftz(M[r] - M2);
+          al[r] = M2 == Mo[r] || Mo[r] == -INFINITY ? 1.f : ex2_ftz(Mo[r] - M2);
+          const float ll = M[r] == Mo[r] ? al[r] : ex2_ftz(M[r] - M2);
           grew |= al[r] != 1.f;
           M[r] = M2;
           // rows without a reference yet have seen nothing: their z are all -inf
-          const float Mu = M2 == -INFINITY ? 0.f : M2, mu = m2 == -INFINITY ? 0.f : m2;
+          const float Mu = M2 == -INFINITY ? 0.f : M2;
           float sum = 0.f;
 #pragma unroll
           for (int g = 0; g < NG; g++) {
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
             for (int k = 0; k < 2; k++) e[g][r][k] = ex2_ftz(fmaf(z[g][n][2 * k + q], c[g], lv[g] - Mu + P_OFF));
             sum = fmaf(e[g][r][0] + e[g][r][1], wl[g], sum);
           }
-          l[r] = fmaf(sum, lvref == -INFINITY ? 0.f : ex2_ftz(Mu - P_OFF - lvref - mu), l[r]);
+          l[r] = fmaf(l[r], ll, sum);
           for (uint32_t b = poison; b; b &= b - 1) {
             const int j = j0 + __ffs(b) - 1;
             if (j >= lo_r[r] && j < hi_r[r]) l[r] = NAN;
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
       for (int o2 = 4; o2 < 32; o2 <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], o2);
       if (r0 == 0) {
         float* s3 = s_stat + (warp * C::ROWS + 8 * (r >> 1) + 2 * t4 + (r & 1)) * 3;
-        s3[0] = m[r]; s3[1] = M[r]; s3[2] = l[r];
+        s3[0] = M[r] == -INFINITY ? -INFINITY : M[r] - P_OFF - lvref; s3[1] = M[r]; s3[2] = l[r];
       }
     }
     // O in its own reference; the readers weigh it

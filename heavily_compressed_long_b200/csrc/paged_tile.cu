@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   rp->valid[lane] =
                       ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
                 if (lane == 0) {
-                  rp->lvref = lvref == -INFINITY ? 0.f : lvref;
+                  rp->lvref = lvref;
                   rp->edge = j0 < im.all_lo || j0 + TILE > im.all_hi || gm != 0xF;
                 }
               }
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_arrive(&q_full[t]);
       }
       const int steps = pair ? n : (n + 1 - t) / 2;
-      float m = -INFINITY, M = -INFINITY, l = 0.f;
+      float m, M = -INFINITY, l = 0.f, lvref = -INFINITY;
       bool sick = false;  // a NaN value in a row that this query sees
       auto look = [&](uint32_t R, int j0) {
         const RoundPar* rp = par + R % PRING;
@@ -683,7 +683,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int q = 0; q < 4; q++) tmem_ld16(tSn + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
         const float4 kc4 = *reinterpret_cast<const float4*>(rp->kc), lv4 = *reinterpret_cast<const float4*>(rp->lv);
         const float4 wl4 = *reinterpret_cast<const float4*>(rp->wl);
-        const float lvref = rp->lvref;
+        const float Mo = M;           // O's reference
+        if (rp->lvref != lvref) {     // (the same for all rows)
+          if (lvref != -INFINITY) grow_lvref(rp->lvref - lvref, l, M);
+          lvref = rp->lvref;
+        }
         const uint32_t vb[2] = {range_mask(j0, lo, hi) & rp->valid[0], range_mask(j0 + 32, lo, hi) & rp->valid[1]};
         const float kc[4] = {fmaxf(kc4.x * back, SCALE_MIN), fmaxf(kc4.y * back, SCALE_MIN),
                              fmaxf(kc4.z * back, SCALE_MIN), fmaxf(kc4.w * back, SCALE_MIN)};
@@ -694,22 +698,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < TILE; j++)
             if (!((vb[j >> 5] >> (j & 31)) & 1u)) sv[j] = 0xFF800000u;  // -inf
         }
-        float mz = -INFINITY, mw = -INFINITY;  // largest z2, largest z2 + lv
+        float mw = -INFINITY;  // largest z2 + lv
 #pragma unroll
         for (int q = 0; q < 4; q++) {
           float sx = fmaxf(__uint_as_float(sv[16 * q]), __uint_as_float(sv[16 * q + 1]));
 #pragma unroll
           for (int j = 2; j < 16; j += 2)
             sx = fmax3(sx, __uint_as_float(sv[16 * q + j]), __uint_as_float(sv[16 * q + j + 1]));
-          const float zx = sx * kc[q];
-          mz = fmaxf(mz, zx);
-          mw = fmaxf(mw, zx + lv[q]);
+          mw = fmaxf(mw, fmaf(sx, kc[q], lv[q]));
         }
-        const float m2 = fmaxf(m, mz);
-        l *= m2 == m ? 1.f : ex2_ftz(m - m2);
-        m = m2;
         const float M2 = mw > M + P_LAZY ? mw : M;
-        const float al = M2 == M || M == -INFINITY ? 1.f : ex2_ftz(M - M2);
+        const float al = M2 == Mo || Mo == -INFINITY ? 1.f : ex2_ftz(Mo - M2);
+        const float ll = M == Mo ? al : ex2_ftz(M - M2);
         M = M2;
         if (__any_sync(0xffffffffu, al != 1.f)) {
           // rescale O, once PV of the last step is done with it (rows without a reference yet are
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int q = 0; q < 2; q++) tmem_st16(tO + 32 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
           }
         }
-        const float Mu = M == -INFINITY ? 0.f : M, mu = m == -INFINITY ? 0.f : m;
+        const float Mu = M == -INFINITY ? 0.f : M;
         // P over the first half of its S, whose scores are in registers
         float lr = 0.f;
 #pragma unroll
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tmem_st16(tSn + 16 * c, pk);
         }
-        l = fmaf(lr, ex2_ftz(Mu - P_OFF - lvref - mu), l);
+        l = fmaf(l, ll, lr);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[2 * t + (n & 1)]);
@@ -770,6 +770,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           look(rg + rr, jfirst + rr * TILE);
         }
       }
+      m = M - P_OFF - lvref;  // (-inf where nothing was seen)
+      if (M == -INFINITY) m = -INFINITY;
       if (sick) l = NAN;
       if (!ok) {
         *s_abort = 1;

@@ -617,3 +617,25 @@ def test_attn_long_rings(hcl, Hkv, G, d, shared, W):
                     None if shared else vs[:, g:g + 1].numpy(), page, 1, W, scale)
             w, wl, mass, zabs = ref.attn(*args)
             assert_attn(ref.f64(out[b:b + 1, h:h + 1]), ref.f64(lse[b:b + 1, h:h + 1]), w, wl, mass, zabs)
+
+
+@pytest.mark.parametrize("G,new,order", [(8, 1, "up"), (8, 1, "down"), (16, 1, "up"), (128, 1, "up"), (128, 1, "down"),
+                                         (8, 60, "up"), (8, 60, "mid")])
+def test_attn_zero_pages_among_others(hcl, G, new, order):
+    """Pages of zero values (scale 2^-126) beside ordinary ones: their rows take their share of the
+    softmax, whatever the order and however the scores lie."""
+    def poison(table, k, ks, v, vs, q):
+        used = table[0][:20]
+        zero = {"up": used[:10], "down": used[10:19], "mid": used[5:13]}[order]
+        v[zero] = 0
+        vs[zero] = 2.0 ** -126
+        if order != "mid":
+            ks[zero] *= 8.0      # the zero rows have the sharper scores
+    got, gl, want, wl, mass, zabs = check_attn(hcl, dict(lens=[319], news=[new], Hkv=1, G=G, d=128, page=16),
+                                               poison=poison, seed=5)
+    # Where the zero rows take all but 2^-60 of a row's sum, the reference M of the other rows'
+    # weights is kept 2^59 / N above where their own largest would put it (the sum is held below
+    # 2^60), and what lies 2^-29 below M is lost in fp16: terms with p * v_scale below
+    # 2^-84 * N * (the largest scale), N = 319 of them: under 2^-60 of the largest value.
+    lost = 2.0 ** -60 * 448 * 2.0 ** -4
+    assert_attn(got, gl, np.where(np.abs(got - want) <= lost, got, want), wl, mass, zabs)
