@@ -164,7 +164,7 @@ hcl_status_t launch_paged_attn(const PagedAttnArgs& a, void* ws, cudaStream_t st
   if (p.G <= ROWS_SMALL) {
     // (small requests have up to 8 rows, unless the call's bounds let them have up to 16)
     const int rows = (int)std::min<long long>(ROWS_SMALL, (long long)std::min(a.max_q, a.T) * p.G);
-    p.n_blocks = rows_blocks(rows, a.kv.d, a.kv.v == nullptr);
+    p.n_blocks = rows_blocks(a.kv.d, a.kv.v == nullptr);
     p.meta = reinterpret_cast<Meta*>(at);
     p.part = reinterpret_cast<float*>(at + meta_bytes(p.n_blocks));
     hcl_status_t e = launch_rows(p, rows, st);

@@ -256,7 +256,7 @@ __device__ __forceinline__ float finish_row(float m, float M, float l, float sin
 // have), and of more; how many blocks each runs with, and the merge of the requests that it split.
 hcl_status_t launch_rows(const Params& p, int rows, cudaStream_t st);
 hcl_status_t launch_tiles(const Params& p, cudaStream_t st);
-int rows_blocks(int rows, int d, bool shared);
+int rows_blocks(int d, bool shared);
 constexpr int ROWS_BLOCKS_MOST = 3;  // of launch_rows, per SM
 int tile_blocks();
 hcl_status_t launch_merge(const Params& p, int rows, cudaStream_t st);

@@ -4,9 +4,10 @@
 // Block: one producer warp and four consumer warps; two or three blocks per SM.  A unit is 64 KV rows of one request and KV head.  The
 // producer copies its codes with TMA (one box per page, or per 64 rows of a longer page) into a
 // ring of swizzled stages and its page scales with 4-byte asynchronous copies that complete on
-// the same mbarrier; page ids are read eight units at a time, eight ahead.  Consumer warps 0, 1
-// take the even units and 2, 3 the odd ones, each 32 rows and its own running softmax, so warps
-// never wait for one another inside an item:
+// the same mbarrier; page ids are read eight units at a time, eight ahead.  With at most 8 query
+// rows consumer warps 0, 1 take the even units and 2, 3 the odd ones, each 32 rows; with 9 to 16
+// every unit goes to all four, warps 0, 1 with the first 8 query rows and 2, 3 with the others.
+// Each has its own running softmax, so warps never wait for one another inside an item:
 //   S^T (16 KV rows x 8 query rows) by m16n8k16 fp16 MMAs: KV rows are the M of the MMA, so up to
 //   8 query rows (a group of 8 heads) waste none of it.  The K fragments come from ldmatrix on
 //   the codes (a 16-byte piece of a row is one k-step, its dimensions taken in the order that
@@ -14,9 +15,9 @@
 //   O^T (16 dimensions x 8 query rows) += V^T P^T from transposed ldmatrix on pairs of codes (a
 //   pair's even and odd dimensions are rows m and m + 8); P^T is S^T's layout transposed
 //   (movmatrix).
-// The bytes bound the kernel once the chain from load to store is covered: with query rows as M,
-// 16 KV rows a warp and step and two blocks, 1.37 GB took 300 us; with 32 KV rows 265 us; this
-// form: see the table of measurements.
+// The bytes bound the kernel once the chain from load to store is covered.  32 requests of up to
+// 32 K rows, 8 KV heads of 8 query heads (1.37 GB, 209 us at the copy rate): 300 us with query
+// rows as M, 16 KV rows a warp and step; 265 us with 32 KV rows; 214 us in this form.
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -31,14 +32,14 @@ constexpr int TILE = 64;               // KV rows per unit
 constexpr int NG = 2;                  // groups of 16 rows (never more than a page) per warp and unit
 constexpr int WPT = TILE / (16 * NG);  // warps per unit
 
-// Blocks per SM: three where the registers (8 query rows) and an even number of stages allow it.
-constexpr int blocks_per_sm(int nt, int d, bool shared) { return nt == 1 && !(d == 128 && !shared) ? 3 : 2; }
+// Blocks per SM: three where an even number of stages leaves the room.
+constexpr int blocks_per_sm(int d, bool shared) { return d == 128 && !shared ? 2 : 3; }
 
-// NT: query rows / 8
-template <int D, bool SHARED, int NT>
+// RH: query rows / 8 that the warps divide among them
+template <int D, bool SHARED, int RH>
 struct Cfg {
-  static constexpr int ROWS = 8 * NT;
-  static constexpr int BLOCKS = blocks_per_sm(NT, D, SHARED);
+  static constexpr int ROWS = 8 * RH;
+  static constexpr int BLOCKS = blocks_per_sm(D, SHARED);
   static constexpr int PLANE = TILE * D;
   static constexpr int STAGE = PLANE * (SHARED ? 1 : 2);
   static constexpr int RING = BLOCKS == 3 ? 49152 : 65536;
@@ -49,9 +50,9 @@ struct Cfg {
   static constexpr int PIECES = D / 16;  // 16-byte pieces of a row = k-steps
   static constexpr int PITCH = D + 4;    // floats of a row in the exchange
   static constexpr uint32_t SCALES = STAGES * STAGE;                    // [STAGES][2][4] floats
-  static constexpr uint32_t MERGE = SCALES + STAGES * 32;               // [NW][ROWS][PITCH] floats
-  static constexpr uint32_t STATS = MERGE + NW * ROWS * PITCH * 4;      // [NW][ROWS][3] floats
-  static constexpr uint32_t BAR = STATS + NW * ROWS * 3 * 4;
+  static constexpr uint32_t MERGE = SCALES + STAGES * 32;               // [NW][8][PITCH] floats
+  static constexpr uint32_t STATS = MERGE + NW * 8 * PITCH * 4;         // [NW][8][3] floats
+  static constexpr uint32_t BAR = STATS + NW * 8 * 3 * 4;
   static constexpr uint32_t SCRATCH = BAR + 2 * STAGES * 8;             // find_share
   static constexpr uint32_t MISC = SCRATCH + (NW + 1 + 4) * 8;
   static constexpr uint32_t TOTAL = MISC + 16;
@@ -135,10 +136,10 @@ __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {
   return true;
 }
 
-template <int D, bool SHARED, int NT>
-__global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
+template <int D, bool SHARED, int RH>
+__global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
     paged_rows_kernel(const Params p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-  using C = Cfg<D, SHARED, NT>;
+  using C = Cfg<D, SHARED, RH>;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);  // (an offset: the compiler still sees shared memory)
   float* s_scale = reinterpret_cast<float*>(sm + C::SCALES);
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; i++) {
       mbar_init(&full[i], 1 + 32);
-      mbar_init(&empty[i], WPT);
+      mbar_init(&empty[i], WPT * RH);
     }
     *s_abort = 0;
     fence_barrier_init();
@@ -243,20 +244,19 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
 
   // -------------------------------------------------------------------- consumers
   // r0: KV row (and + 8) of a score, even / odd dimension pair of an output, query row of a Q
-  // fragment; this thread's query rows: 8 n + 2 t4 + e, n < NT, e < 2
+  // fragment; this thread's query rows: row0 + 2 t4 + e, e < 2
   const int r0 = lane >> 2, t4 = lane & 3;
-  constexpr int NR = 2 * NT;
+  const int row0 = RH == 2 ? 8 * (warp >> 1) : 0;
   uint32_t it = 0;
   bool ok = true;
   do {
     const int nrows = w.r.nq * p.G;
-    // Q rows r0 + 8 n (row = query * G + head), dims 16c + 4 t4 .. + 3 of every piece
-    uint32_t qf[C::PIECES][NT][2];
-    float back[NR];
-    int hi_r[NR], lo_r[NR];
-#pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const int row = r0 + 8 * n;
+    // Q row row0 + r0 (row = query * G + head), dims 16c + 4 t4 .. + 3 of every piece
+    uint32_t qf[C::PIECES][2];
+    float back[2];
+    int hi_r[2], lo_r[2];
+    {
+      const int row = row0 + r0;
       const bool valid = row < nrows;
       const int i = valid ? p.by_G.div(row) : 0, head = w.g * p.G + (valid ? row - i * p.G : 0);
       const uint2* src = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.a.q) +
@@ -277,16 +277,16 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
       float bk;
       const float f = row_factor(am, &bk);
 #pragma unroll
-      for (int e = 0; e < 2; e++) back[2 * n + e] = __shfl_sync(~0u, bk, (2 * t4 + e) * 4);
+      for (int e = 0; e < 2; e++) back[e] = __shfl_sync(~0u, bk, (2 * t4 + e) * 4);
 #pragma unroll
       for (int c = 0; c < C::PIECES; c++) {
-        qf[c][n][0] = half2_of(__uint_as_float(x[c].x << 16) * f, __uint_as_float(x[c].x & 0xFFFF0000u) * f);
-        qf[c][n][1] = half2_of(__uint_as_float(x[c].y << 16) * f, __uint_as_float(x[c].y & 0xFFFF0000u) * f);
+        qf[c][0] = half2_of(__uint_as_float(x[c].x << 16) * f, __uint_as_float(x[c].x & 0xFFFF0000u) * f);
+        qf[c][1] = half2_of(__uint_as_float(x[c].y << 16) * f, __uint_as_float(x[c].y & 0xFFFF0000u) * f);
       }
     }
 #pragma unroll
-    for (int r = 0; r < NR; r++) {
-      const int row = 8 * (r >> 1) + 2 * t4 + (r & 1);
+    for (int r = 0; r < 2; r++) {
+      const int row = row0 + 2 * t4 + r;
       const bool valid = row < nrows;
       const int i = valid ? p.by_G.div(row) : 0;
       hi_r[r] = valid ? vis_hi(p, w.r, i) : 0;
@@ -296,23 +296,21 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
     const int all_lo = vis_lo(p, w.r, w.r.nq - 1), all_hi = vis_hi(p, w.r, 0);
     const int any_lo = vis_lo(p, w.r, 0), any_hi = vis_hi(p, w.r, w.r.nq - 1);
 
-    float o[C::PIECES][NT][4];  // dims 16 c + 2 r0 (+ 1 for the last two), query rows of n (e = k & 1)
+    float o[C::PIECES][4];  // dims 16 c + 2 r0 (+ 1 for the last two), query row e = k & 1
 #pragma unroll
     for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
-      for (int n = 0; n < NT; n++)
-#pragma unroll
-        for (int k = 0; k < 4; k++) o[c][n][k] = 0.f;
+      for (int k = 0; k < 4; k++) o[c][k] = 0.f;
     const int rows0 = (warp % WPT) * 16 * NG;  // this warp's rows of a tile
-    float M[NR], l[NR], lvref = -INFINITY;
+    float M[2], l[2], lvref = -INFINITY;
 #pragma unroll
-    for (int r = 0; r < NR; r++) {
+    for (int r = 0; r < 2; r++) {
       M[r] = -INFINITY;
       l[r] = 0.f;
     }
 
     for (int i = 0; i < w.count; i++, it++) {
-      if (it % (NW / WPT) != warp / WPT) continue;
+      if (RH == 1 && it % (NW / WPT) != warp / WPT) continue;
       const int st = it % C::STAGES;
       ok = mbar_wait(&full[st], (it / C::STAGES) & 1, p.limit, s_abort);
       ok = __all_sync(~0u, ok);
@@ -326,14 +324,12 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
         const uint32_t vb = kb + (SHARED ? 0 : C::PLANE);
         // rows (lane & 15) of a group, piece (lane >> 4) of two
         const int frow = lane & 15, fpiece = lane >> 4;
-        // S^T: z[g][n][k]: KV row 16 g + r0 + 8 (k >> 1), query row 8 n + 2 t4 + (k & 1)
-        float z[NG][NT][4];
+        // S^T: z[g][k]: KV row 16 g + r0 + 8 (k >> 1), query row e = k & 1
+        float z[NG][4];
 #pragma unroll
         for (int g = 0; g < NG; g++)
 #pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int k = 0; k < 4; k++) z[g][n][k] = 0.f;
+          for (int k = 0; k < 4; k++) z[g][k] = 0.f;
 #pragma unroll
         for (int c = 0; c < C::PIECES; c += 2)
 #pragma unroll
@@ -344,44 +340,35 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
             for (int u = 0; u < 2; u++) {
               const uint32_t a[4] = {half2_of_codes(uint16_t(r[2 * u])), half2_of_codes(uint16_t(r[2 * u + 1])),
                                      half2_of_codes(uint16_t(r[2 * u] >> 16)), half2_of_codes(uint16_t(r[2 * u + 1] >> 16))};
-#pragma unroll
-              for (int n = 0; n < NT; n++) mma16816(z[g][n], a, qf[c + u][n][0], qf[c + u][n][1]);
+              mma16816(z[g], a, qf[c + u][0], qf[c + u][1]);
             }
           }
         uint32_t poison = 0;  // a bit for each of the KV rows
         static_assert(16 * NG <= 32, "poison");
-        if (j0 < all_lo || j0 + 16 * NG > all_hi || !(ks[0] > 0.f) || !(ks[NG - 1] > 0.f)) {
+        const bool edge = j0 < all_lo || j0 + 16 * NG > all_hi || !(ks[0] > 0.f) || !(ks[NG - 1] > 0.f);
+        if (edge) {
           // some query row does not see some of these KV rows, or a group has no page
 #pragma unroll
           for (int g = 0; g < NG; g++)
 #pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-              for (int k = 0; k < 4; k++) {
-                const int j = j0 + g * 16 + r0 + 8 * (k >> 1), r = 2 * n + (k & 1);
-                if (j < lo_r[r] || j >= hi_r[r] || !(ks[g] > 0.f)) z[g][n][k] = -INFINITY;
-              }
-          // NaN codes among the values would reach the rows that do not see them (0 * NaN), and
-          // rows behind the last (or of no page) hold anything: they become 0, and `poison` says
-          // which KV rows had one
-          __syncwarp();
-          uint8_t* vp = sm + st * C::STAGE + (SHARED ? 0 : C::PLANE) + rows0 * D;
+            for (int k = 0; k < 4; k++) {
+              const int j = j0 + g * 16 + r0 + 8 * (k >> 1), r = k & 1;
+              if (j < lo_r[r] || j >= hi_r[r] || !(ks[g] > 0.f)) z[g][k] = -INFINITY;
+            }
+          // NaN codes among the values would reach the query rows that do not see them (0 * NaN),
+          // and rows behind the last (or of no page) hold anything: below they are taken as 0, and
+          // `poison` says which KV rows had one
+          const uint8_t* vp = sm + st * C::STAGE + (SHARED ? 0 : C::PLANE) + rows0 * D;
 #pragma unroll
           for (int g = 0; g < NG; g++)
 #pragma unroll
             for (int i2 = 0; i2 < C::PIECES / 2; i2++) {
               const int e = i2 * 32 + lane;  // piece of the group
-              uint4* at = reinterpret_cast<uint4*>(vp + g * 16 * D + e * 16);
-              const uint4 v = *at;
-              const uint4 n4 = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
-              if (n4.x | n4.y | n4.z | n4.w) {
-                *at = make_uint4(v.x & ~n4.x, v.y & ~n4.y, v.z & ~n4.z, v.w & ~n4.w);
-                if (ks[g] > 0.f) poison |= 1u << (g * 16 + e / C::PIECES);
-              }
+              const uint4 v = *reinterpret_cast<const uint4*>(vp + g * 16 * D + e * 16);
+              if (ks[g] > 0.f && (nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w)))
+                poison |= 1u << (g * 16 + e / C::PIECES);
             }
           poison = __reduce_or_sync(~0u, poison);
-          fence_proxy_async_smem();
-          __syncwarp();
         }
         float lv[NG], wl[NG], kc[NG];
         const float lvold = lvref;
@@ -396,13 +383,13 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
           lv[g] = ks[g] > 0.f ? fmaxf(lv[g], lvref - LV_SPAN) : lvref;
           wl[g] = ks[g] > 0.f ? ex2_ftz(lvref - lv[g]) : 0.f;
         }
-        float Mo[NR];  // O's reference
+        float Mo[2];  // O's reference
 #pragma unroll
-        for (int r = 0; r < NR; r++) Mo[r] = M[r];
+        for (int r = 0; r < 2; r++) Mo[r] = M[r];
         if (lvref != lvold && lvold != -INFINITY) {  // (the same in all lanes)
           // (l lies over the eight lanes of a row: their M must move alike)
 #pragma unroll
-          for (int r = 0; r < NR; r++) {
+          for (int r = 0; r < 2; r++) {
             float big = l[r];
 #pragma unroll
             for (int o2 = 4; o2 < 32; o2 <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o2));
@@ -411,16 +398,15 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
             if (was != -INFINITY) l[r] *= exp2f(lvref - lvold - (M[r] - was));
           }
         }
-        float al[NR], e[NG][NR][2];
+        float al[2], e[NG][2][2];
         bool grew = false;
 #pragma unroll
-        for (int r = 0; r < NR; r++) {
-          const int n = r >> 1, q = r & 1;
+        for (int r = 0; r < 2; r++) {
           float c[NG], mw = -INFINITY;  // largest z2 + lv
 #pragma unroll
           for (int g = 0; g < NG; g++) {
             c[g] = fmaxf(kc[g] * back[r], SCALE_MIN);
-            mw = fmaxf(mw, fmaf(fmaxf(z[g][n][q], z[g][n][2 + q]), c[g], lv[g]));
+            mw = fmaxf(mw, fmaf(fmaxf(z[g][r], z[g][2 + r]), c[g], lv[g]));
           }
 #pragma unroll
           for (int o2 = 4; o2 < 32; o2 <<= 1) mw = fmaxf(mw, __shfl_xor_sync(~0u, mw, o2));
@@ -435,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
 #pragma unroll
           for (int g = 0; g < NG; g++) {
 #pragma unroll
-            for (int k = 0; k < 2; k++) e[g][r][k] = ex2_ftz(fmaf(z[g][n][2 * k + q], c[g], lv[g] - Mu + P_OFF));
+            for (int k = 0; k < 2; k++) e[g][r][k] = ex2_ftz(fmaf(z[g][2 * k + r], c[g], lv[g] - Mu + P_OFF));
             sum = fmaf(e[g][r][0] + e[g][r][1], wl[g], sum);
           }
           l[r] = fmaf(l[r], ll, sum);
@@ -444,20 +430,16 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
             if (j >= lo_r[r] && j < hi_r[r]) l[r] = NAN;
           }
         }
-        uint32_t pb[NG][NT][2];  // P^T fragments
+        uint32_t pb[NG][2];  // P^T fragments
 #pragma unroll
         for (int g = 0; g < NG; g++)
 #pragma unroll
-          for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int k = 0; k < 2; k++) pb[g][n][k] = transpose8(half2_of(e[g][2 * n][k], e[g][2 * n + 1][k]));
+          for (int k = 0; k < 2; k++) pb[g][k] = transpose8(half2_of(e[g][0][k], e[g][1][k]));
         if (__any_sync(~0u, grew)) {
 #pragma unroll
           for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
-            for (int n = 0; n < NT; n++)
-#pragma unroll
-              for (int k = 0; k < 4; k++) o[c][n][k] *= al[2 * n + (k & 1)];
+            for (int k = 0; k < 4; k++) o[c][k] *= al[k & 1];
         }
         // O^T += V^T P^T: pieces c, c + 1 per ldmatrix
 #pragma unroll
@@ -466,14 +448,17 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
           for (int g = 0; g < NG; g++) {
             uint32_t r[4];
             ldsm4t(vb + piece<D>(g * 16 + frow, c + fpiece), r);
+            if (edge) {
+#pragma unroll
+              for (int i2 = 0; i2 < 4; i2++) r[i2] &= ~nan_bytes(r[i2]);
+            }
 #pragma unroll
             for (int u = 0; u < 2; u++) {
               // bytes (row 2t dim 2n, row 2t dim 2n+1, row 2t+1 dim 2n, row 2t+1 dim 2n+1)
               const uint32_t x0 = __byte_perm(r[2 * u], 0, 0x3120), x1 = __byte_perm(r[2 * u + 1], 0, 0x3120);
               const uint32_t a[4] = {half2_of_codes(uint16_t(x0)), half2_of_codes(uint16_t(x0 >> 16)),
                                      half2_of_codes(uint16_t(x1)), half2_of_codes(uint16_t(x1 >> 16))};
-#pragma unroll
-              for (int n = 0; n < NT; n++) mma16816(o[c + u][n], a, pb[g][n][0], pb[g][n][1]);
+              mma16816(o[c + u], a, pb[g][0], pb[g][1]);
             }
           }
       }
@@ -486,11 +471,11 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
     }
     // join the warps: l's partial sums lie over the eight threads of a query row
 #pragma unroll
-    for (int r = 0; r < NR; r++) {
+    for (int r = 0; r < 2; r++) {
 #pragma unroll
       for (int o2 = 4; o2 < 32; o2 <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], o2);
       if (r0 == 0) {
-        float* s3 = s_stat + (warp * C::ROWS + 8 * (r >> 1) + 2 * t4 + (r & 1)) * 3;
+        float* s3 = s_stat + (warp * 8 + 2 * t4 + r) * 3;
         s3[0] = M[r] == -INFINITY ? -INFINITY : M[r] - P_OFF - lvref; s3[1] = M[r]; s3[2] = l[r];
       }
     }
@@ -498,9 +483,9 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
 #pragma unroll
     for (int c = 0; c < C::PIECES; c++)
 #pragma unroll
-      for (int r = 0; r < NR; r++)
-        *reinterpret_cast<float2*>(s_merge + (warp * C::ROWS + 8 * (r >> 1) + 2 * t4 + (r & 1)) * C::PITCH + c * 16 + 2 * r0) =
-            make_float2(o[c][r >> 1][r & 1], o[c][r >> 1][2 + (r & 1)]);
+      for (int r = 0; r < 2; r++)
+        *reinterpret_cast<float2*>(s_merge + (warp * 8 + 2 * t4 + r) * C::PITCH + c * 16 + 2 * r0) =
+            make_float2(o[c][r], o[c][2 + r]);
     // (a warp whose wait ran out ends the block here, at the same item for all four)
     uint32_t gone;
     asm volatile(
@@ -517,21 +502,24 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
 #pragma unroll
       for (int k = 0; k < C::ROWS * TPR / (NW * 32); k++) {
         const int row = tid / TPR + k * (NW * 32 / TPR);
+        // the warps that had this row
+        constexpr int NV = NW / RH;
+        const int v0 = (RH == 2 ? (row >> 3) * NV : 0) * 8 + (row & 7);
         float mt = -INFINITY, Mt = -INFINITY, lt = 0.f;
 #pragma unroll
-        for (int v = 0; v < NW; v++) {
-          const float* s3 = s_stat + (v * C::ROWS + row) * 3;
+        for (int v = 0; v < NV; v++) {
+          const float* s3 = s_stat + (v0 + v * 8) * 3;
           mt = fmaxf(mt, s3[0]);
           Mt = fmaxf(Mt, s3[1]);
         }
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < NW; v++) {
-          const float* s3 = s_stat + (v * C::ROWS + row) * 3;
+        for (int v = 0; v < NV; v++) {
+          const float* s3 = s_stat + (v0 + v * 8) * 3;
           lt += s3[0] == -INFINITY ? s3[2] : s3[2] * ex2_ftz(s3[0] - mt);
           const float f = s3[1] == -INFINITY ? 0.f : ex2_ftz(s3[1] - Mt);
           if (f != 0.f) {
-            const float4 x = *reinterpret_cast<const float4*>(s_merge + (v * C::ROWS + row) * C::PITCH + col);
+            const float4 x = *reinterpret_cast<const float4*>(s_merge + (v0 + v * 8) * C::PITCH + col);
             a.x = fmaf(x.x, f, a.x); a.y = fmaf(x.y, f, a.y); a.z = fmaf(x.z, f, a.z); a.w = fmaf(x.w, f, a.w);
           }
         }
@@ -555,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, NT>::BLOCKS))
   } while (walk_next(p, w));
 }
 
-template <int D, bool SHARED, int NT>
+template <int D, bool SHARED, int RH>
 hcl_status_t launch_t(const Params& p, cudaStream_t st) {
   CUtensorMap tk, tv;
   const int box = std::min(p.a.kv.page, TILE);
@@ -566,8 +554,8 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
     e = code_map(&tv, p.a.kv.v, p.a.kv, box, true);
     if (e != HCL_OK) return e;
   }
-  using C = Cfg<D, SHARED, NT>;
-  auto kern = paged_rows_kernel<D, SHARED, NT>;
+  using C = Cfg<D, SHARED, RH>;
+  auto kern = paged_rows_kernel<D, SHARED, RH>;
   const int smem = (int)C::TOTAL + 1024;
   static_assert(C::BLOCKS * (C::TOTAL + 2048) <= 233472, "blocks per SM");
   e = set_kernel_attrs(reinterpret_cast<const void*>(kern), smem, false);
@@ -578,8 +566,8 @@ hcl_status_t launch_t(const Params& p, cudaStream_t st) {
 
 }  // namespace
 
-int rows_blocks(int rows, int d, bool shared) {
-  return std::min(1024, blocks_per_sm(rows <= 8 ? 1 : 2, d, shared) * num_sms());
+int rows_blocks(int d, bool shared) {
+  return std::min(1024, blocks_per_sm(d, shared) * num_sms());
 }
 
 hcl_status_t launch_rows(const Params& p, int rows, cudaStream_t st) {

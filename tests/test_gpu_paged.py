@@ -404,7 +404,8 @@ def test_attn_query_range(hcl, G, new):
 
 
 @pytest.mark.parametrize("G,news,shared", [(8, [1, 1], False), (128, [1, 1], True), (16, [60, 80], True),
-                                           (8, [100, 30], False)])
+                                           (8, [100, 30], False), (4, [4, 3], True), (4, [4, 3], False),
+                                           (2, [4, 1], True), (1, [7, 4], False)])
 def test_attn_nan_row_reaches_only_those_who_see_it(hcl, G, news, shared):
     """A NaN code in a key or value row: the queries that see the row become NaN, no others."""
     lens, page = [120, 100], 16
