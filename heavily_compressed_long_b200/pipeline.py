@@ -1,7 +1,9 @@
 """Composition of the hot-path calls for the three workload shapes, on caller-provided CUDA
 tensors: a CSA decode step, an HCA layer (prefill chunk or decode), and a CSA/HCA layer pair
-over a chunked prefill.  Owns the intermediate buffers (scores, indices, workspaces) so a step
+over a chunked prefill; and for ragged batches the page bookkeeping of a batch and the layers over
+its paged 8-bit caches.  Owns the intermediate buffers (scores, indices, workspaces) so a step
 allocates nothing; every step is a sequence of libhcl calls on one stream."""
+import contextlib
 import math
 
 import torch
@@ -171,3 +173,94 @@ class PairPrefill:
         if api.hca_dense_attn_workspace_bytes(*self.q_hca.shape[:3], self.Nh, self.W):
             n += 1
         return n
+
+
+class PagedBatch:
+    """The page bookkeeping of a ragged batch, shared by all layers whose caches hold the same rows:
+    block tables, free pages and, for each step, slots and positions of the new rows.
+
+    B requests of up to max_pages pages of `page` rows, n_pages pages in all; T: the most new rows
+    of a step.  Nothing here reads the device back, so a step can be captured and replayed."""
+
+    def __init__(self, B, page, max_pages, n_pages, T, device="cuda"):
+        def i32(*shape, value=0):
+            return torch.full(shape, value, dtype=torch.int32, device=device)
+
+        self.B, self.page, self.T = B, page, T
+        self.seq_len, self.start = i32(B), i32(B)
+        self.table = i32(B, max_pages, value=-1)
+        self.free_list = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.n_free = i32(1, value=n_pages)
+        self.cu_new, self.pos, self.slot = i32(B + 1), i32(T), i32(T)
+        self.status = i32(1)
+
+    def plan(self, new_len, keep=None, stream=None):
+        """One step: of each request keep[b] rows stay (default: all; 0 for a new request in the
+        row) and new_len[b] rows (int32 [B]) are added.  Afterwards start holds the first new
+        row's position, slot and pos the new rows' places (-1 behind the last), seq_len the
+        lengths.  The status word has HCL_ERR_NO_PAGES where a request did not get its rows."""
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            self.start.copy_(self.seq_len if keep is None else keep)
+        api.hcl_page_plan(self.start, new_len, self.seq_len, self.table, self.free_list, self.n_free,
+                          self.page, self.cu_new, self.pos, self.slot, status=self.status,
+                          stream=stream)
+
+
+class PagedAttnLayer:
+    """One attention layer over a paged 8-bit cache: the step's new rows are written, then its
+    queries attend (causal; with W only over the last W rows; with m over entries of m tokens).
+
+    shared: rows are both key and value (H query heads on Hkv of them)."""
+
+    def __init__(self, batch: PagedBatch, n_pages, H, Hkv, d, shared=False, m=1, W=0, sink=None,
+                 device="cuda"):
+        self.batch, self.m, self.W, self.sink, self.H = batch, m, W, sink, H
+        self.store = api.PagedKV.empty(n_pages, Hkv, batch.page, d, shared=shared, device=device)
+        n = api.paged_attn_workspace_bytes(batch.T, H, Hkv, d)
+        self.ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+    def write(self, k_new, v_new=None, stream=None):
+        """k_new, v_new bf16 [T, Hkv, d], the rows of the batch's last plan."""
+        api.hcl_paged_write(k_new, v_new, self.batch.slot, self.store, status=self.batch.status,
+                            stream=stream)
+
+    def attend(self, q, out, lse=None, max_q=None, cu_q=None, q_start=None, sink=None, stream=None):
+        """q bf16 [T, H, d]: the plan's new rows, unless cu_q and q_start say otherwise."""
+        b = self.batch
+        return api.hcl_paged_attn(q, b.cu_new if cu_q is None else cu_q,
+                                  b.start if q_start is None else q_start, self.store, b.table,
+                                  b.seq_len, out, lse=lse, m=self.m, W=self.W, max_q=max_q,
+                                  sink=self.sink if sink is None else sink, ws=self.ws,
+                                  status=b.status, stream=stream)
+
+    def step(self, q, k_new, v_new, out, lse=None, max_q=None, stream=None):
+        self.write(k_new, v_new, stream=stream)
+        return self.attend(q, out, lse=lse, max_q=max_q, stream=stream)
+
+
+class PagedHcaLayer:
+    """HCA attention of a ragged batch over two paged 8-bit caches: the compressed entries (mh
+    tokens each, dense) and the raw rows (a sliding window of W), whose partial results merge by
+    log-sum-exp with the sink.  Rows are both key and value, one for all H heads.
+
+    raw and entries are PagedBatch's, planned for tokens and for completed entries; the rows of
+    both are written with raw_layer.write and entry_layer.write before attend."""
+
+    def __init__(self, raw: PagedBatch, entries: PagedBatch, n_raw_pages, n_entry_pages, H, d, mh=128,
+                 W=128, sink=None, device="cuda"):
+        self.raw, self.entries, self.sink = raw, entries, sink
+        self.raw_layer = PagedAttnLayer(raw, n_raw_pages, H, 1, d, shared=True, W=W, device=device)
+        self.entry_layer = PagedAttnLayer(entries, n_entry_pages, H, 1, d, shared=True, m=mh,
+                                          device=device)
+        # (rows of no request are left as they were: zeros, which merge to zeros)
+        self.o_parts = torch.zeros(2, raw.T, H, d, dtype=torch.bfloat16, device=device)
+        self.lse_parts = torch.full((2, raw.T, H), -math.inf, dtype=torch.float32, device=device)
+
+    def attend(self, q, out, lse=None, max_q=None, stream=None):
+        """q bf16 [T, H, d], the raw batch's new rows (T: its capacity)."""
+        b = self.raw
+        for i, layer in enumerate((self.entry_layer, self.raw_layer)):
+            layer.attend(q, self.o_parts[i], lse=self.lse_parts[i], max_q=max_q, cu_q=b.cu_new,
+                         q_start=b.start, stream=stream)
+        api.hcl_lse_merge(self.o_parts, self.lse_parts, out, lse_out=lse, sink=self.sink, stream=stream)
+        return out

@@ -640,3 +640,134 @@ def test_attn_zero_pages_among_others(hcl, G, new, order):
     # 2^-84 * N * (the largest scale), N = 319 of them: under 2^-60 of the largest value.
     lost = 2.0 ** -60 * 448 * 2.0 ** -4
     assert_attn(got, gl, np.where(np.abs(got - want) <= lost, got, want), wl, mass, zabs)
+
+
+# ------------------------------------------------------------------------------------ together
+
+
+def held_rows(b, layer, r):
+    """The rows that the layer's cache holds for request r, as values (float64)."""
+    n = b.seq_len[r].item()
+    ids = b.table[r, :-(-n // b.page)].cpu().numpy()
+
+    def plane(codes, scale):
+        v = ref.decode_e4m3(codes.cpu().numpy()[ids]) * scale.cpu().numpy()[ids].astype(np.float64)[:, :, None, None]
+        return v.transpose(0, 2, 1, 3).reshape(-1, v.shape[1], v.shape[3])[:n]
+
+    s = layer.store
+    return plane(s.k, s.k_scale), (None if s.v is None else plane(s.v, s.v_scale))
+
+
+@pytest.mark.parametrize("page,d,Hkv,G,graph", [(16, 128, 2, 8, False), (64, 64, 1, 4, True)])
+def test_serving_steps(hcl, page, d, Hkv, G, graph):
+    """Prompts, decode steps (captured and replayed in the second case), rejected drafts and a
+    request that takes another's place: plan, write and attention as a server calls them.  The
+    cache follows the rows that were written, the attention follows the cache."""
+    from heavily_compressed_long_b200.pipeline import PagedAttnLayer, PagedBatch
+    gen = torch.Generator().manual_seed(page)
+    B, T, H = 4, 160, Hkv * G
+    b = PagedBatch(B, page, 20, 4 * 20, T)
+    layer = PagedAttnLayer(b, 4 * 20, H, Hkv, d)
+    rows = [np.zeros((0, 2, Hkv, d)) for _ in range(B)]  # what was written
+    out, lse = torch.zeros(T, H, d, dtype=torch.bfloat16, device=DEV), torch.zeros(T, H, device=DEV)
+    q, k, v = (torch.zeros(T, h, d, dtype=torch.bfloat16, device=DEV) for h in (H, Hkv, Hkv))
+    d_new, d_keep = i32([0] * B), i32([0] * B)
+
+    def calls(max_q):
+        b.plan(d_new, d_keep)
+        layer.step(q, k, v, out, lse=lse, max_q=max_q)
+
+    captured = None
+    steps = [([0] * 4, [40, 1, 70, 17])] + [(None, [1, 1, 1, 1])] * 4 + [(None, [3, 0, 4, 1]), ("less", [2, 1, 1, 1]),
+                                                                       ("replace", [1, 30, 1, 2])]
+    for keep, new in steps:
+        lens = [len(r) for r in rows]
+        keep_n = (list(keep) if isinstance(keep, list) else [max(0, n - 2) for n in lens] if keep == "less"
+                  else [lens[0], 0, lens[2], lens[3]] if keep == "replace" else lens)
+        d_new.copy_(i32(new))
+        d_keep.copy_(i32(keep_n))
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=gen).to(torch.bfloat16))
+        if graph and keep is None and new == [1] * 4:
+            if captured is None:
+                captured = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(captured):
+                    calls(1)
+            captured.replay()
+        else:
+            calls(max(new))
+        assert b.status.item() == 0
+        at = 0
+        kv = np.stack([ref.f64(k), ref.f64(v)], 1)
+        for r in range(B):
+            rows[r] = np.concatenate([rows[r][:keep_n[r]], kv[at:at + new[r]]])
+            at += new[r]
+        assert b.seq_len.tolist() == [len(r) for r in rows]
+        cu = np.concatenate([[0], np.cumsum(new)])
+        for r in range(B):
+            kk, vv = held_rows(b, layer, r)
+            # a code is within half a step of its value at the page's scale, and was rounded once
+            # more at most per growth of the scale for values near the subnormals: 2^-4 of the value
+            # or two subnormal half steps, 2 * 2^-10 of the scale (<= 2 * amax / 448, amax < 8)
+            for got, want in ((kk, rows[r][:, 0]), (vv, rows[r][:, 1])):
+                assert np.all(np.abs(got - want) <= 2.0 ** -4 * np.abs(want) + 2 * 2.0 ** -10 * 16 / 448)
+        tab = b.table.cpu().numpy()
+        w, wl, mass, zabs = ref.attn(ref.f64(q), cu, keep_n, b.seq_len.tolist(), np.maximum(tab, 0),
+                                     layer.store.k.cpu().numpy(), layer.store.k_scale.cpu().numpy(),
+                                     layer.store.v.cpu().numpy(), layer.store.v_scale.cpu().numpy(), page, 1, 0,
+                                     1 / math.sqrt(d))
+        n = int(cu[-1])
+        assert_attn(ref.f64(out)[:n], ref.f64(lse)[:n], w[:n], wl[:n], mass[:n], zabs[:n])
+
+
+def test_paged_hca_layer_against_oracle(hcl, orc):
+    """HCA over paged entries and a paged raw window: compress, plan, write, attend, merge, against
+    the oracle's HCA attention over the rows that the caches hold."""
+    from heavily_compressed_long_b200.pipeline import PagedBatch, PagedHcaLayer
+    gen = torch.Generator().manual_seed(21)
+    lens, news, H, d, mh, W = [1500, 700], [5, 1], 16, 128, 128, 128
+    B, T = 2, 8
+    raw, ent = PagedBatch(B, 64, 24, 50, 2200), PagedBatch(B, 16, 2, 6, 20)
+    q_raw = PagedBatch(B, 64, 24, 50, T)  # the step's plan: the same state, fewer rows
+    sink = torch.randn(H, generator=gen)
+    kv = [torch.randn(1, n, d, generator=gen).to(torch.bfloat16).cuda() for n in lens]
+    gate = [torch.randn(1, n, d, generator=gen).to(torch.bfloat16).cuda() for n in lens]
+    bias = (torch.randn(mh, generator=gen) * 0.1).cuda()
+    done = [n // mh for n in lens]  # completed entries
+    entries = []
+    for i in range(B):
+        e = torch.empty(1, -(-lens[i] // mh), d, dtype=torch.bfloat16, device=DEV)
+        hcl.hcl_hca_compress(kv[i], gate[i], bias, mh, e)
+        entries.append(e[0, :done[i]])
+    layer = PagedHcaLayer(q_raw, ent, 50, 6, H, d, mh=mh, W=W, sink=sink.cuda())
+    # everything but the step's rows, then the step's rows
+    raw.plan(i32([n - m for n, m in zip(lens, news)]))
+    first = torch.zeros(2200, 1, d, dtype=torch.bfloat16, device=DEV)
+    first[:sum(lens) - sum(news), 0] = torch.cat([x[0, :n - m] for x, n, m in zip(kv, lens, news)])
+    hcl.hcl_paged_write(first, None, raw.slot, layer.raw_layer.store)
+    q_raw.seq_len, q_raw.table, q_raw.free_list, q_raw.n_free = raw.seq_len, raw.table, raw.free_list, raw.n_free
+    q_raw.plan(i32(news))
+    step = torch.zeros(T, 1, d, dtype=torch.bfloat16, device=DEV)
+    step[:sum(news), 0] = torch.cat([x[0, n - m:] for x, n, m in zip(kv, lens, news)])
+    layer.raw_layer.write(step)
+    ent.plan(i32(done))
+    e_rows = torch.zeros(20, 1, d, dtype=torch.bfloat16, device=DEV)
+    e_rows[:sum(done), 0] = torch.cat(entries)
+    layer.entry_layer.write(e_rows)
+    q = torch.randn(T, H, d, generator=gen).to(torch.bfloat16)
+    out, lse = torch.empty(T, H, d, dtype=torch.bfloat16, device=DEV), torch.empty(T, H, device=DEV)
+    layer.attend(q.cuda(), out, lse=lse, max_q=max(news))
+    assert q_raw.status.item() == 0 and ent.status.item() == 0 and raw.status.item() == 0
+    at = 0
+    for i in range(B):
+        rr, _ = held_rows(q_raw, layer.raw_layer, i)
+        ee, _ = held_rows(ent, layer.entry_layer, i)
+        as16 = lambda x: torch.from_numpy(x[None, :, 0].astype(np.float32)).to(torch.bfloat16)  # noqa: E731  (exact)
+        pos = torch.arange(lens[i] - news[i], lens[i], dtype=torch.int32)[None]
+        o, l = orc.hca_attn(q[at:at + news[i]][None], orc.KV(0, as16(ee), done[i]), done[i], mh,
+                            orc.KV(0, as16(rr), lens[i]), W, pos, sink=sink)
+        # the framework's bound for attention over 8-bit rows; log-sum-exps: scores of bf16 queries
+        # and exact rows
+        assert np.abs(ref.f64(out)[at:at + news[i]] - o[0]).max() <= 2e-2
+        assert np.abs(ref.f64(lse)[at:at + news[i]] - l[0]).max() <= 1e-3
+        at += news[i]
