@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
 // chunk.  Prompts have one run per page of rows, a decode step one per row: the chunk is the
 // page when that gives blocks enough to fill the GPU, less otherwise, down to one row.
 
-constexpr int PW_THREADS = 256;
+constexpr int PW_THREADS = 128;  // (65 us for 64 K rows x 8 heads x 2 planes; 256 threads 73, 512 103)
 
 __device__ __forceinline__ uint32_t bf2_absmax(uint32_t a, uint32_t b) {  // b: sign bits clear; NaN loses
   uint32_t r;
@@ -209,7 +209,8 @@ __global__ void __launch_bounds__(PW_THREADS) paged_write_kernel(PagedWriteArgs 
   constexpr int PIECES = D / 8;  // per row
   __shared__ int s_len;
   __shared__ uint32_t s_begin[4];
-  __shared__ float s_max[PW_THREADS / 32];
+  __shared__ float s_max[2][PW_THREADS / 32];  // (by turns: one barrier a run)
+  int turn = 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int plane = blockIdx.y / p.kv.Hkv, g = blockIdx.y % p.kv.Hkv;
   const int page = p.kv.page;
@@ -241,24 +242,32 @@ __global__ void __launch_bounds__(PW_THREADS) paged_write_kernel(PagedWriteArgs 
     if (mask == 0) { c |= 31; continue; }
     c += __ffs(mask) - 1;
     const int t0 = t_lo + c, slot = p.slot[t0], off = slot & (page - 1);
-    // the run's length: rows t0 + i with slot + i, up to the page's end
+    // The run: rows t0 + i with slot + i, up to the page's end.  Its rows are loaded while its
+    // length is checked: all that the page has room for, where the next row continues it.
     const int most = min(page - off, p.T - t0);
-    __syncthreads();
-    if (tid == 0) s_len = most;
-    __syncthreads();
-    if (tid < most && p.slot[t0 + tid] != slot + tid) atomicMin(&s_len, tid);
-    __syncthreads();
-    const int n = s_len;
-    // the rows, and their largest magnitude
+    const int guess = most > 1 && p.slot[t0 + 1] == slot + 1 ? most : 1;
+    const size_t pg = (size_t)(slot >> sh) * p.kv.Hkv + g;
+    const float was = off ? scales[pg] : 0.f;
     uint4 x[NP];
     uint32_t am = 0;
 #pragma unroll
     for (int i = 0; i < NP; i++) {
       const int e = i * PW_THREADS + tid;
       x[i] = make_uint4(0, 0, 0, 0);
-      if (e < n * PIECES)
+      if (e < guess * PIECES)
         x[i] = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)(t0 + e / PIECES) * stride +
                                                     g * D + (e % PIECES) * 8));
+    }
+    int n = guess;
+    if (guess > 1 && !__syncthreads_and(tid >= most || p.slot[t0 + tid] == slot + tid)) {
+      if (tid == 0) s_len = most;
+      __syncthreads();
+      if (tid < most && p.slot[t0 + tid] != slot + tid) atomicMin(&s_len, tid);
+      __syncthreads();
+      n = s_len;
+#pragma unroll
+      for (int i = 0; i < NP; i++)
+        if (i * PW_THREADS + tid >= n * PIECES) x[i] = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < NP; i++)
@@ -280,11 +289,10 @@ __global__ void __launch_bounds__(PW_THREADS) paged_write_kernel(PagedWriteArgs 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-    if (lane == 0) s_max[warp] = amax;
-    const size_t pg = (size_t)(slot >> sh) * p.kv.Hkv + g;
-    const float was = off ? scales[pg] : 0.f;
+    turn ^= 1;
+    if (lane == 0) s_max[turn][warp] = amax;
     __syncthreads();
-    amax = s_max[lane & (PW_THREADS / 32 - 1)];
+    amax = s_max[turn][lane & (PW_THREADS / 32 - 1)];
 #pragma unroll
     for (int o = PW_THREADS / 64; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
     const float s = fmaxf(pow2_scale(amax), was);
@@ -364,14 +372,15 @@ hcl_status_t launch_paged_write(const PagedWriteArgs& a, cudaStream_t st) {
   while (chunk > 1 && (a.T + chunk - 1) / chunk * planes < 8ll * num_sms()) chunk >>= 1;
   const int np = std::max(1, a.kv.page * a.kv.d / 8 / PW_THREADS);
   if (a.kv.d == 128) {
-    if (np == 1) return write_t<128, 1>(a, sh, chunk, st);
     if (np == 2) return write_t<128, 2>(a, sh, chunk, st);
     if (np == 4) return write_t<128, 4>(a, sh, chunk, st);
-    return write_t<128, 8>(a, sh, chunk, st);
+    if (np == 8) return write_t<128, 8>(a, sh, chunk, st);
+    return write_t<128, 16>(a, sh, chunk, st);
   }
   if (np == 1) return write_t<64, 1>(a, sh, chunk, st);
   if (np == 2) return write_t<64, 2>(a, sh, chunk, st);
-  return write_t<64, 4>(a, sh, chunk, st);
+  if (np == 4) return write_t<64, 4>(a, sh, chunk, st);
+  return write_t<64, 8>(a, sh, chunk, st);
 }
 
 }  // namespace hcl
