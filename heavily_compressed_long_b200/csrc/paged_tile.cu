@@ -316,9 +316,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
       for (int q = 0; q < NQ; q++)
         x[q] = *reinterpret_cast<const uint4*>(sm + src0 + su * (TILE * D) + q * C::RPP * D);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&u_empty[su]);
-      u++;
       if (edge) {
         // Not every query row sees the whole round: NaN codes become 0 (0 * NaN would reach rows
         // that do not see them; rows behind the last hold anything) and are noted for the softmax
@@ -345,6 +342,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         *reinterpret_cast<uint4*>(tile + second + q * C::RPP * 128) = pc & 4 ? lo : hi;
       }
       fence_proxy_async_smem();
+      // The unit is released only behind the stores that needed its values: a load that was issued
+      // before an arrival may still read after it, and find the next unit's bytes.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&u_empty[su]);
+      u++;
     };
     for (uint32_t it = 0;; it++) {
       ok = ok && mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
@@ -463,8 +465,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         ok = __all_sync(~0u, mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort));
         const Item im = items[it % IRING];
         if (!ok || im.count == 0) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
         const int32_t* trow = p.a.table + (size_t)im.b * p.a.max_pages;
         // the page of this lane's group in round i: -2 where no row is wanted
         auto page_at = [&](int i) {
@@ -525,6 +525,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           id = id1; id1 = id2; ks = ks1; vs = vs1;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
       }
       if (!ok) {
         *s_abort = 1;

@@ -771,3 +771,42 @@ def test_paged_hca_layer_against_oracle(hcl, orc):
         assert np.abs(ref.f64(out)[at:at + news[i]] - o[0]).max() <= 2e-2
         assert np.abs(ref.f64(lse)[at:at + news[i]] - l[0]).max() <= 1e-3
         at += news[i]
+
+
+@pytest.mark.parametrize("d,page,shared", [(128, 64, False), (128, 16, False), (64, 64, False), (128, 64, True)])
+def test_attn_same_bits_under_load(hcl, d, page, shared):
+    """Calls in flight behind one another, on caches too large to stay in L2 together: the same bits
+    every time (a read that came too late once took the next rows' bytes)."""
+    B, n, Hkv, G = 3, 3000, 4, 8
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    sets = []
+    for _ in range(2):
+        per = -(-n // page)
+        shape = (B * per, Hkv, page, d)
+
+        def plane():
+            x = torch.randn(shape, generator=gen, device=DEV, dtype=torch.float16).mul_(100).clamp_(-448, 448)
+            return x.to(torch.float8_e4m3fn).view(torch.uint8), torch.full((B * per, Hkv), 2.0 ** -6, device=DEV)
+
+        k, ks = plane()
+        store = hcl.PagedKV(k, ks) if shared else hcl.PagedKV(k, ks, *plane())
+        table = torch.randperm(B * per, generator=gen, device=DEV).to(torch.int32).view(B, per)
+        q = torch.randn(B * n, Hkv * G, d, generator=gen, device=DEV).to(torch.bfloat16)
+        sets.append((q, store, table, torch.empty_like(q)))
+    cu, start, lens = i32([0, n, 2 * n, 3 * n]), i32([0] * B), i32([n] * B)
+    ws = [torch.empty(hcl.paged_attn_workspace_bytes(B * n, Hkv * G, Hkv, d), dtype=torch.uint8, device=DEV)
+          for _ in sets]
+
+    def call(i):
+        q, store, table, out = sets[i]
+        hcl.hcl_paged_attn(q, cu, start, store, table, lens, out, max_q=n, ws=ws[i])
+
+    call(0)
+    torch.cuda.synchronize()
+    first = sets[0][3].clone()
+    for _ in range(25):
+        call(0)
+        call(1)
+        call(0)
+        torch.cuda.synchronize()
+        assert torch.equal(sets[0][3], first)
