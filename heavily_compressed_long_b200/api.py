@@ -4,6 +4,7 @@ Every function takes CUDA tensors (device memory owned by the caller) and enqueu
 corresponding libhcl call on the current torch stream (or `stream`).  No arithmetic of the
 method happens here.  Formats: HCL_BF16 / HCL_FP32 / HCL_FP8SPLIT / HCL_MXFP4.
 """
+import contextlib
 import ctypes
 import math
 
@@ -256,7 +257,7 @@ def _rows(t, name, dev, heads, d):
     s = t.stride()
     if s[2] != 1 or (heads > 1 and s[1] != d):
         raise ValueError(f"{name}: the heads of a token must lie together")
-    return t.data_ptr(), (s[0] if t.shape[0] > 1 else max(s[0], heads * d))
+    return t.data_ptr(), (s[0] if t.shape[0] > 1 else heads * d)
 
 
 class PagedKV:
@@ -338,9 +339,9 @@ def hcl_paged_attn(q, cu_q, q_start, store: PagedKV, table, kv_len, out, lse=Non
     if ws is None:
         need = paged_attn_workspace_bytes(T, H, store.Hkv, d)
         if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                ws.record_stream(stream)
+            # (from the launching stream's pool: a block of another stream's may still be in use there)
+            with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+                ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be contiguous, on the current CUDA device")
     check(lib().hcl_paged_attn(

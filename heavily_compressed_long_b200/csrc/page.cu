@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
   if (tid == 0) { s_rows[p.B] = tot.rows; s_back[p.B] = tot.back; s_need[p.B] = tot.need; }
   int nfree = *p.n_free;
   if (nfree < 0 || nfree > p.n_pages) { nfree = nfree < 0 ? 0 : p.n_pages; fault = HCL_ERR_DEVICE_FAULT; }
-  const int top = min(nfree + tot.back, p.n_pages);  // free pages after the releases
+  const int top = (int)min((long long)nfree + tot.back, (long long)p.n_pages);  // free pages after the releases
   __syncthreads();
 
   // releases: the r-th released page goes to place top - 1 - r of the stack
@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
     if (r < top) p.free_list[top - 1 - r] = id;
     else fault = HCL_ERR_DEVICE_FAULT;
   }
+  __syncwarp();
   if (gridDim.x > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
@@ -123,10 +124,11 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
   }
 
   // A request gets its rows when they fit the table, end within T, and the free pages reach for
-  // it and all before it.  `rows`: its new rows as given.
+  // it and all before it.  (Where the row sums are saturated a request that needs pages shows no
+  // rows; it ends beyond T.)
   auto admitted = [&](int b) {
     const int nw = s_rows[b + 1] - s_rows[b], need = s_need[b + 1] - s_need[b];
-    if (nw == 0) return true;
+    if (nw == 0 && need == 0) return true;
     return (long long)s_keep[b] + nw <= room && s_rows[b + 1] <= p.T &&
            (need == 0 || s_need[b + 1] <= top);
   };

@@ -89,8 +89,9 @@ __device__ __forceinline__ int vis_lo(const Params& p, const Req& r, int i) {
 
 __device__ __forceinline__ Req load_req(const Params& p, int b, bool say) {
   Req r;
-  int c0 = __ldg(p.a.cu_q + b), c1 = __ldg(p.a.cu_q + b + 1), len = __ldg(p.a.kv_len + b);
-  r.qs = __ldg(p.a.q_start + b);
+  // (plain loads: a read-only one could be moved to before the wait for the kernel that wrote them)
+  int c0 = p.a.cu_q[b], c1 = p.a.cu_q[b + 1], len = p.a.kv_len[b];
+  r.qs = p.a.q_start[b];
   const long long room = (long long)p.a.max_pages << p.sh;
   int fault = 0;
   if (c0 < 0 || c1 < c0 || c1 > p.a.T || c1 - c0 > p.a.max_q) {

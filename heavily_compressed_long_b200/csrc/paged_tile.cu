@@ -143,8 +143,8 @@ __device__ __forceinline__ bool walk_first(const Params& p, const Share& s, int 
   w.tile = tile;
   w.r = load_req(p, b, false);
   w.nt = rounds_of(p, w.r, tile, &w.j0);
-  w.g = (int)s.rem / (ITEM_COST + w.nt);
-  walk_set(w, (int)s.rem - w.g * (ITEM_COST + w.nt));
+  w.g = (int)(s.rem / (ITEM_COST + w.nt));
+  walk_set(w, (int)(s.rem % (ITEM_COST + w.nt)));
   return true;
 }
 __device__ __forceinline__ bool walk_next(const Params& p, Walk& w) {

@@ -252,13 +252,16 @@ class PagedHcaLayer:
         self.raw_layer = PagedAttnLayer(raw, n_raw_pages, H, 1, d, shared=True, W=W, device=device)
         self.entry_layer = PagedAttnLayer(entries, n_entry_pages, H, 1, d, shared=True, m=mh,
                                           device=device)
-        # (rows of no request are left as they were: zeros, which merge to zeros)
         self.o_parts = torch.zeros(2, raw.T, H, d, dtype=torch.bfloat16, device=device)
-        self.lse_parts = torch.full((2, raw.T, H), -math.inf, dtype=torch.float32, device=device)
+        self.lse_parts = torch.empty(2, raw.T, H, dtype=torch.float32, device=device)
 
     def attend(self, q, out, lse=None, max_q=None, stream=None):
-        """q bf16 [T, H, d], the raw batch's new rows (T: its capacity)."""
+        """q bf16 [T, H, d], the raw batch's new rows (T: its capacity).  Rows of out behind the
+        last request's become zeros."""
         b = self.raw
+        # rows that belong to no request, or to one only in an earlier step, weigh nothing
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            self.lse_parts.fill_(-math.inf)
         for i, layer in enumerate((self.entry_layer, self.raw_layer)):
             layer.attend(q, self.o_parts[i], lse=self.lse_parts[i], max_q=max_q, cu_q=b.cu_new,
                          q_start=b.start, stream=stream)

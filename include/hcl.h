@@ -419,7 +419,8 @@ HCL_API hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const 
  * sees may count as zero in out (never in lse).  Pages outside
  * the cache, and rows beyond max_pages * page, are left out: HCL_ERR_DEVICE_FAULT.  Rows at or
  * behind kv_len, and pages that no query of the request sees, are not read into the result,
- * whatever their codes.
+ * whatever their codes.  A NaN code reaches only queries that see its row: in a key it makes out
+ * and lse NaN, in a value out in its dimension and, at some places in a page, the others and lse.
  * Supported: H a multiple of Hkv, H / Hkv <= 128, B <= 8192, max_pages * page <= 2^30.  The result is bitwise
  * reproducible for the same lengths; it may depend on the other requests of the batch, whose
  * lengths set where a long request is split.

@@ -103,6 +103,20 @@ def test_plan_beyond_capacity_and_width(hcl):
     assert w["status"] == 16 and w["seq"] == [20, 4, 2, 2]
 
 
+def test_plan_row_sums_beyond_every_capacity(hcl):
+    """New rows that sum far past T (and past 32 bits): the requests that end there get nothing, also
+    one whose own few rows would fit; no page is taken for it from an empty stack."""
+    rng = np.random.default_rng(8)
+    S = PlanState(5, 3, 2, 16, 40, rng)
+    big = 2 ** 31 - 1
+    w = S.step(hcl, [0] * 5, [10, big, 10, big, 1])
+    assert w["status"] == 32 and w["seq"] == [10, 0, 0, 0, 0] and S.d_n.item() == 1
+    w = S.step(hcl, S.seq, [0, 20, 2 ** 30, 20, 5])
+    assert w["status"] == 32 and w["seq"] == [10, 0, 0, 0, 0]
+    w = S.step(hcl, S.seq, [big, big, 0, 0, 0])
+    assert w["status"] == 32 and w["seq"] == [10, 0, 0, 0, 0]
+
+
 def test_plan_no_requests_no_rows(hcl):
     empty = torch.zeros(0, dtype=torch.int32, device=DEV)
     cu, pos, slot = i32([7]), i32([5, 5]), i32([5, 5])
@@ -771,6 +785,38 @@ def test_paged_hca_layer_against_oracle(hcl, orc):
         assert np.abs(ref.f64(out)[at:at + news[i]] - o[0]).max() <= 2e-2
         assert np.abs(ref.f64(lse)[at:at + news[i]] - l[0]).max() <= 1e-3
         at += news[i]
+
+
+def test_paged_hca_layer_fewer_rows_in_a_later_step(hcl):
+    """Rows behind the last request's become zeros, whatever an earlier and longer step left."""
+    from heavily_compressed_long_b200.pipeline import PagedBatch, PagedHcaLayer
+    gen = torch.Generator().manual_seed(5)
+    B, T, H, d = 2, 12, 16, 128
+    raw, ent = PagedBatch(B, 16, 8, 16, T), PagedBatch(B, 16, 2, 4, T)
+    layer = PagedHcaLayer(raw, ent, 16, 4, H, d, mh=128, W=128)
+    ent.plan(i32([0, 0]))
+    out = torch.empty(T, H, d, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(T, H, device=DEV)
+    for news in ([7, 5], [1, 2]):
+        raw.plan(i32(news))
+        layer.raw_layer.write(torch.randn(T, 1, d, generator=gen).to(torch.bfloat16).cuda())
+        layer.attend(torch.randn(T, H, d, generator=gen).to(torch.bfloat16).cuda(), out, lse=lse, max_q=max(news))
+        n = sum(news)
+        assert torch.isfinite(lse[:n]).all() and (out[:n] != 0).any(-1).all()
+        assert (out[n:] == 0).all() and torch.isneginf(lse[n:]).all()
+
+
+def test_one_row_of_any_stride(hcl):
+    """A single row's token stride does not matter."""
+    gen = torch.Generator().manual_seed(6)
+    wide = torch.randn(1, 2 * 64 + 3, generator=gen).to(torch.bfloat16).cuda()
+    x = wide[:, :128].unflatten(1, (2, 64))
+    a, b = (hcl.PagedKV.empty(1, 2, 16, 64, shared=True) for _ in range(2))
+    out = [torch.empty(1, 2, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    for store, rows, o in ((a, x, out[0]), (b, x.contiguous(), out[1])):
+        hcl.hcl_paged_write(rows, None, i32([0]), store)
+        hcl.hcl_paged_attn(rows, i32([0, 1]), i32([0]), store, i32([[0]]), i32([1]), o)
+    assert torch.equal(a.k[:, :, 0], b.k[:, :, 0]) and torch.equal(*out)
 
 
 @pytest.mark.parametrize("d,page,shared", [(128, 64, False), (128, 16, False), (64, 64, False), (128, 64, True)])
