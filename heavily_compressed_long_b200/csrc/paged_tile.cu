@@ -184,14 +184,16 @@ struct Cfg {
   static constexpr uint32_t QT = 128 * D * 2;         // bytes of a Q tile
   static constexpr uint32_t KT = TILE * D * 2;        // bytes of a K or V tile
   static constexpr uint32_t HALF = TILE * 128;        // its two halves of 64 dimensions
-  static constexpr int NK = SHARED ? 8 : 4;           // K (or shared) tiles in the ring
+  static constexpr int NK = SHARED ? 6 : 3;           // K (or shared) tiles in the ring
   static constexpr int NV = NK;
   static constexpr uint32_t K = 2 * QT;
   static constexpr uint32_t V = SHARED ? K : K + NK * KT;
-  static constexpr uint32_t STAGE = K + 8 * KT;
-  static constexpr uint32_t PAR = STAGE + NU * TILE * D;
-  static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [128][4] floats (single mode)
-  static constexpr uint32_t ITEMS = STAT + 128 * 16;
+  static constexpr uint32_t STAGE = K + 6 * KT;
+  static constexpr uint32_t OUT = STAGE + NU * TILE * D;              // [8 warps][32 rows][128 bytes]
+  static constexpr uint32_t PAR = OUT + 8 * 4096;
+  static constexpr uint32_t STAT = PAR + PRING * sizeof(RoundPar);    // [2][128][4] floats (single mode)
+  static constexpr uint32_t BACK = STAT + 2 * 128 * 16;               // [ITEM] floats: the query rows' factors
+  static constexpr uint32_t ITEMS = BACK + ITEM * 4;
   static constexpr uint32_t BAR = ITEMS + IRING * sizeof(Item);
   static constexpr int NBAR = 2 * NK + 2 * NV + 3 * 4 + 2 + 1 + 2 * IRING + 2 * NU;
   static constexpr uint32_t SCRATCH = BAR + NBAR * 8;
@@ -217,7 +219,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* s_full = v_empty + C::NV;        // [tile][buffer] S of a step in TMEM
   uint64_t* p_full = s_full + 4;             // [tile][buffer] P in TMEM, O rescaled
   uint64_t* o_done = s_full + 8;             // [tile][buffer] PV of a step completed
-  uint64_t* q_full = s_full + 12;            // [tile] Q tile in shared memory
+  uint64_t* q_full = s_full + 12;            // the item's Q tiles and their factors stand
+  uint64_t* q_empty = s_full + 13;           // its scores are all computed, its factors read
   uint64_t* drain = s_full + 14;
   uint64_t* i_full = s_full + 15;            // [IRING] an item's description stands
   uint64_t* i_empty = i_full + IRING;        // [IRING] every role is done with it
@@ -230,9 +233,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < C::NK; i++) { mbar_init(&k_full[i], 128); mbar_init(&k_empty[i], 2); }
     for (int i = 0; i < C::NV; i++) { mbar_init(&v_full[i], 128); mbar_init(&v_empty[i], 2); }
     for (int i = 0; i < 4; i++) { mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 128); mbar_init(&o_done[i], 1); }
-    for (int t = 0; t < 2; t++) {
-      mbar_init(&q_full[t], 128);
-    }
+    mbar_init(q_full, 128);
+    mbar_init(q_empty, 2 + 8);
     mbar_init(drain, 2);
     for (int i = 0; i < IRING; i++) { mbar_init(&i_full[i], 1); mbar_init(&i_empty[i], 4 + 8 + 2 + 1); }
     for (int i = 0; i < C::NU; i++) { mbar_init(&u_full[i], 1); mbar_init(&u_empty[i], 4); }
@@ -306,6 +308,45 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t first = dst0 + (((pc & 4 ? c0 + 1 : c0) ^ sw) << 4), second = dst0 + (((pc & 4 ? c0 : c0 + 1) ^ sw) << 4);
     bool ok = true;
     uint32_t rg = 0, u = 0;  // rounds, staging units so far
+    // Q rows of an item, bf16, to their places in the Q tiles (rows behind the last: zeros)
+    auto load_q = [&](const Item* im) {
+      constexpr int LPR = D / 8;  // 16-byte pieces of a row
+      const int rows = im->rows, n = rows > 128 ? ITEM : 128, w0 = tid - 256, pq = w0 % LPR;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)im->c0 * p.a.q_stride + im->g * p.G * D + pq * 8;
+#pragma unroll 4
+      for (int r = w0 / LPR; r < n; r += 128 / LPR) {
+        const int qr = im->row0 + min(r, rows - 1), qi = p.by_G.div(qr);
+        const uint32_t dst = smem_u32(sm) + (r >> 7) * C::QT + (pq >> 3) * 16384 + (r & 127) * 128 + (((pq & 7) ^ (r & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                     "l"(q + qi * p.a.q_stride + (qr - qi * p.G) * D), "r"(r < rows ? 16 : 0)
+                     : "memory");
+      }
+    };
+    // this thread's row of Q tile t to fp16 with its exponent taken out
+    auto convert_q = [&](int t) {
+      const int r = tid - 256;
+      uint8_t* qrow = sm + t * C::QT + r * 128;
+      uint32_t top = 0;  // (of magnitudes, whose bits order as their values do; NaN above all)
+#pragma unroll
+      for (int e = 0; e < D / 8; e++) {
+        const uint4 x = *reinterpret_cast<const uint4*>(qrow + (e >> 3) * 16384 + (((e & 7) ^ (r & 7)) << 4));
+        top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
+                       __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+      }
+      float back;
+      const float f = row_factor(__uint_as_float(max(top & 0xFFFFu, top >> 16) << 16), &back);
+      reinterpret_cast<float*>(sm + C::BACK)[t * 128 + r] = back;
+#pragma unroll 4
+      for (int e = 0; e < D / 8; e++) {
+        uint4* at = reinterpret_cast<uint4*>(qrow + (e >> 3) * 16384 + (((e & 7) ^ (r & 7)) << 4));
+        const uint4 x = *at;
+        uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          a[k] = half2_of(__uint_as_float(a[k] << 16) * f, __uint_as_float(a[k] & 0xFFFF0000u) * f);
+        *at = make_uint4(a[0], a[1], a[2], a[3]);
+      }
+    };
     // one staging unit into `tile`
     auto widen = [&](uint8_t* tile, RoundPar* rp, bool mark) {
       constexpr int NQ = TILE / C::RPP;
@@ -351,8 +392,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (uint32_t it = 0;; it++) {
       ok = ok && mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
       ok = !bar_or(2, 128, !ok);  // the four warps go on, or end, together
-      const int count = ok ? items[it % IRING].count : 0;
+      const Item* im = items + it % IRING;
+      const int count = ok ? im->count : 0;
       if (count == 0) break;
+      // The item's Q rows go to shared memory as they are, while its first round is widened, and
+      // are turned to fp16 in place.
+      if (it > 0) ok = mbar_wait(q_empty, (it - 1) & 1, p.limit, s_abort);
+      ok = !bar_or(2, 128, !ok);
+      if (!ok) break;
+      const int rows = im->rows, qtiles = rows > 128 ? 2 : 1;
+      load_q(im);
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_empty[it % IRING]);
       for (int i = 0; i < count && ok; i++, rg++) {
@@ -366,6 +415,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (rg >= C::NV) ok = ok && mbar_wait(&v_empty[vb], ((rg / C::NV) & 1) ^ 1, p.limit, s_abort);
           widen(sm + C::V + vb * C::KT, rp, true);
           mbar_arrive(&v_full[vb]);
+        }
+        if (i == 0) {  // (all four warps come here, whatever their waits said)
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("bar.sync 5, 128;" ::: "memory");
+          for (int t = 0; t < qtiles; t++) convert_q(t);
+          fence_proxy_async_smem();
+          mbar_arrive(q_full);
         }
       }
     }
@@ -385,8 +441,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t dk = (((sbase + C::K) & 0x3FFFFu) >> 4) | (1u << 16);
       const uint32_t dv = (((sbase + C::V) & 0x3FFFFu) >> 4) | ((C::HALF >> 4) << 16);
       constexpr uint32_t idS = idesc_f16(128, TILE), idPV = idesc_f16(128, D) | (1u << 16);
-      // rg: rounds before this item; n: this tile's steps before this one; qp: parity of the items
-      uint32_t rg = 0, n = 0, qp = 0;
+      // rg: rounds before this item; n: this tile's steps before this one
+      uint32_t rg = 0, n = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait(bar, parity, p.limit, s_abort); };
       // Both issuers release a K or V tile; where one of them alone uses it, it does so twice.
@@ -394,9 +450,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         commit_lead(bar, lead);
         if (alone) commit_lead(bar, lead);
       };
-      // scores of round R, this tile's step s, with the Q tile at aq
-      auto issue_s = [&](uint32_t R, uint32_t s, uint32_t aq, bool alone) {
+      // scores of round R, this tile's step s, with the Q tile at aq; `last` of the item.  They go
+      // where P of the step before the last was: its PV must have completed.
+      auto issue_s = [&](uint32_t R, uint32_t s, uint32_t aq, bool alone, bool last) {
         const uint32_t kb = R % C::NK;
+        if (s > 1) wait(&o_done[2 * t + (s & 1)], ((s - 2) >> 1) & 1);
         wait(&k_full[kb], (R / C::NK) & 1);
         if (!ok) return;
         tc_fence_after();
@@ -406,6 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           umma_ss(d, aq + ((ks >> 2) * (16384 >> 4) + (ks & 3) * 2), b0 + ((ks >> 2) * (C::HALF >> 4) + (ks & 3) * 2), idS,
                   ks > 0 ? 1u : 0u, lead);
         commit_lead(&s_full[2 * t + (s & 1)], lead);
+        if (last) commit_lead(q_empty, lead);
         if (!SHARED) release(&k_empty[kb], alone);
       };
       for (uint32_t it = 0;; it++) {
@@ -419,19 +478,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         // this tile's step k is round k (pair) or 2k + t (single)
         const int steps = pair ? count : (count + 1 - t) / 2;
         const uint32_t aq = pair && t ? dq + (C::QT >> 4) : dq, stride = pair ? 1 : 2;
-        // both, in every item: a barrier whose last phase was not waited for could still be in it,
-        // and show the one before, of the wanted parity (group 1 arrives in single mode too)
-        wait(&q_full[0], qp);
-        wait(&q_full[1], qp);
-        qp ^= 1;
+        wait(q_full, it & 1);
         uint32_t R = rg + (pair ? 0 : t);
-        if (steps > 0) issue_s(R, n, aq, !pair);
+        if (steps > 0) issue_s(R, n, aq, !pair, steps == 1);
+        else if (lane == 0) mbar_arrive(q_empty);
         for (int k = 0; k < steps && ok; k++, R += stride, n++) {
-          // the next step's scores go where P of the last step was: its PV must have completed
-          if (k + 1 < steps) {
-            if (k > 0) wait(&o_done[2 * t + ((n & 1) ^ 1)], ((n - 1) >> 1) & 1);
-            issue_s(R + stride, n + 1, aq, !pair);
-          }
+          if (k + 1 < steps) issue_s(R + stride, n + 1, aq, !pair, k + 2 == steps);
           const uint32_t vb = R % C::NV;
           if (!SHARED) wait(&v_full[vb], (R / C::NV) & 1);
           wait(&p_full[2 * t + (n & 1)], (n >> 1) & 1);
@@ -595,7 +647,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (uint32_t it = 0;; it++) {
       const Item* im = items + it % IRING;
-      ok = mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
+      ok = ok && mbar_wait(&i_full[it % IRING], (it / IRING) & 1, p.limit, s_abort);
+      if (ok && im->count) ok = mbar_wait(q_full, it & 1, p.limit, s_abort);
       if (bar_or(3, 256, !ok)) { ok = false; break; }
       const int n = im->count, rows = im->rows, jfirst = im->j0;
       if (n == 0) break;
@@ -603,57 +656,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int irow = (pair ? t * 128 : 0) + row;  // row of the item
       const bool valid = irow < rows;
       int hi, lo;
-      size_t orow;
-      int head;
+      int head, orow;  // (T * H < 2^31)
       {
         const int qr = im->row0 + (valid ? irow : 0), qi = p.by_G.div(qr);
         const Req r = {0, im->c0, im->len, im->qs};
         hi = valid ? vis_hi(p, r, qi) : 0;
         lo = valid ? vis_lo(p, r, qi) : 0;
         head = im->g * p.G + qr - qi * p.G;
-        orow = (size_t)(r.c0 + qi) * p.a.H + head;
+        orow = (r.c0 + qi) * p.a.H + head;
       }
-      // Q rows -> fp16 with their exponents taken out, D / 8 lanes a row (in single mode group 1
-      // only needs the factors)
-      float back = 1.f;
-      {
-        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an instruction
-        const int wrow = (pair ? t * 128 : 0) + (warp & 3) * 32, sub = lane / LPR, piece = lane % LPR;
-        uint4 x[32 / RPI];
-#pragma unroll
-        for (int i = 0; i < 32 / RPI; i++) {
-          const int ir = wrow + i * RPI + sub;
-          const int qr = im->row0 + min(ir, rows - 1), qi = p.by_G.div(qr);
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(im->c0 + qi) * p.a.q_stride +
-                                     (im->g * p.G + qr - qi * p.G) * D;
-          x[i] = ir < rows ? __ldg(reinterpret_cast<const uint4*>(src) + piece) : make_uint4(0, 0, 0, 0);
-        }
-        uint8_t* qt = sm + t * C::QT;
-#pragma unroll
-        for (int i = 0; i < 32 / RPI; i++) {
-          uint32_t a[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          float am = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; k++)
-            am = fmax3(am, fabsf(__uint_as_float(a[k] << 16)), fabsf(__uint_as_float(a[k] & 0xFFFF0000u)));
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) am = fmaxf(am, __shfl_xor_sync(~0u, am, o));
-          float bk;
-          const float f = row_factor(am, &bk);
-          const float mine = __shfl_sync(~0u, bk, (lane % RPI) * LPR);
-          if (lane / RPI == i) back = mine;  // (lane r owns row r of the warp)
-          if (pair || t == 0) {
-            const int r = (warp & 3) * 32 + i * RPI + sub;
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-              a[k] = half2_of(__uint_as_float(a[k] << 16) * f, __uint_as_float(a[k] & 0xFFFF0000u) * f);
-            *reinterpret_cast<uint4*>(qt + (piece >> 3) * 16384 + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
-                make_uint4(a[0], a[1], a[2], a[3]);
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[t]);
-      }
+      const float back = reinterpret_cast<const float*>(sm + C::BACK)[irow];
       const int steps = pair ? n : (n + 1 - t) / 2;
       float m, M = -INFINITY, l = 0.f, lvref = -INFINITY;
       bool sick = false;  // a NaN value in a row that this query sees
@@ -761,6 +773,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[2 * t + (n & 1)]);
+        if (k == 0) {  // (behind the use of the factor)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_empty);
+        }
+      }
+      if (steps == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty);
       }
       if (ok && steps > 0) {
         const uint32_t n = step + steps - 1;
@@ -779,116 +799,99 @@ __global__ void __launch_bounds__(THREADS, 1)
         *s_abort = 1;
         report(p.a.status, HCL_ERR_TIMEOUT);
       }
-      // both groups are done with their MMAs (Q's shared memory is free), or the block ends here
-      if (bar_or(3, 256, !ok)) { ok = false; break; }
+      // Single mode: the groups join their results, each reading both O's (the same lanes of TMEM)
+      // for its half of the dimensions.
+      float fa = 1.f, fb = 0.f;  // factors of the (first) O and the other group's
+      if (!pair) {
+        *reinterpret_cast<float4*>(s_stat + (t * 128 + row) * 4) = make_float4(m, M, l, 0.f);
+        tc_fence_before();
+        if (bar_or(3, 256, !ok)) { ok = false; break; }
+        tc_fence_after();
+        const float4 s0 = *reinterpret_cast<const float4*>(s_stat + row * 4);
+        const float4 s1 = *reinterpret_cast<const float4*>(s_stat + (128 + row) * 4);
+        m = fmaxf(s0.x, s1.x);
+        M = fmaxf(s0.y, s1.y);
+        l = (s0.x == -INFINITY ? s0.z : s0.z * ex2_ftz(s0.x - m)) + (s1.x == -INFINITY ? s1.z : s1.z * ex2_ftz(s1.x - m));
+        fa = s0.y == -INFINITY ? 0.f : ex2_ftz(s0.y - M);
+        fb = s1.y == -INFINITY ? 0.f : ex2_ftz(s1.y - M);
+      }
+      if (!ok) continue;  // (to the barrier where the block's end is agreed)
       const bool whole = im->whole != 0;
       float* pp = p.part + (2 * (size_t)blockIdx.x + (im->head ? 0 : 1)) * part_floats(ITEM, D);
-      float mine = 1.f, other = 0.f;  // factors of this group's O and, in single mode, group 1's
-      float* ex = reinterpret_cast<float*>(sm);  // single mode: O of group 1, swizzled [128][D]
-      if (!pair) {
-        if (t == 1) {
-          *reinterpret_cast<float4*>(s_stat + row * 4) = make_float4(m, M, l, 0.f);
-#pragma unroll
-          for (int q = 0; q < D / 16; q++) {
-            uint32_t r16[16];
-            tmem_ld16(tO + q * 16, r16);
-            tmem_ld_wait();
-            if (steps > 0) {
-#pragma unroll
-              for (int j = 0; j < 16; j += 4)
-                *reinterpret_cast<uint4*>(ex + row * D + (((q * 4 + (j >> 2)) ^ (row & 7)) << 2)) =
-                    make_uint4(r16[j], r16[j + 1], r16[j + 2], r16[j + 3]);
-            }
-          }
-        }
-        asm volatile("bar.sync 4, 256;" ::: "memory");
-        if (t == 0) {
-          const float4 s4 = *reinterpret_cast<const float4*>(s_stat + row * 4);
-          const float mt = fmaxf(m, s4.x), Mt = fmaxf(M, s4.y);
-          l = (m == -INFINITY ? l : l * ex2_ftz(m - mt)) + (s4.x == -INFINITY ? s4.z : s4.z * ex2_ftz(s4.x - mt));
-          mine = M == -INFINITY ? 0.f : ex2_ftz(M - Mt);
-          other = s4.y == -INFINITY ? 0.f : ex2_ftz(s4.y - Mt);
-          m = mt;
-          M = Mt;
-        }
+      if (whole) {
+        float lse;
+        const float f = finish_row(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
+        fa *= f;
+        fb *= f;
+        if (valid && p.a.lse && (pair || t == 0)) p.a.lse[orow] = lse;
+      } else if (pair || t == 0) {
+        *reinterpret_cast<float4*>(pp + irow * 4) = make_float4(m, M, l, 0.f);
       }
-      if (pair || t == 0) {
-        float f = 1.f, lse = 0.f;
-        if (whole) {
-          f = finish_row(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
-          if (valid && p.a.lse) p.a.lse[orow] = lse;
-        } else {
-          *reinterpret_cast<float4*>(pp + irow * 4) = make_float4(m, M, l, 0.f);
-        }
-        // 64 dimensions at a time: a row's values go through shared memory (the row's own place,
-        // where Q or the exchange was), so that the warp writes whole rows
-        const int wr = (warp & 3) * 32;
-        uint8_t* stage = sm + (pair ? t * C::QT : 0);
-        const uint32_t pitch = pair ? D * 2 : D * 4;
+      // 64 dimensions at a time, through shared memory, so that the warp writes whole rows: lanes
+      // 8 i .. 8 i + 7 write the 8 pieces of 16 bytes of row 4 k + i
+      uint8_t* stage = sm + C::OUT + warp * 4096;
+      uint8_t* mine = stage + lane * 128;
+      const int r_in = lane >> 3, e_in = lane & 7, irow0 = irow - lane;
+#pragma unroll 1
+      for (int c = pair ? 0 : t; c < (pair ? D / 64 : min(t + 1, D / 64)); c++) {
+        float x[64];
+        const uint32_t at = (pair ? tO : tO - t * 128) + 64 * c;
 #pragma unroll
-        for (int c = 0; c < D / 64; c++) {
-          float x[64];
+        for (int q = 0; q < 4; q++)
+          tmem_ld16(at + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(&x[16 * q])));
+        tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 4; q++)
-            tmem_ld16(tO + 64 * c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(&x[16 * q])));
-          tmem_ld_wait();
+        for (int j = 0; j < 64; j++) x[j] = fa == 0.f ? 0.f : x[j] * fa;
+        if (!pair) {
 #pragma unroll
-          for (int j = 0; j < 64; j++) x[j] = mine == 0.f ? 0.f : x[j] * mine;
-          if (other != 0.f) {
+          for (int q = 0; q < 4; q++) {
+            uint32_t y[16];
+            tmem_ld16(at + 128 + 16 * q, y);
+            tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(ex + row * D + (((c * 16 + (j >> 2)) ^ (row & 7)) << 2));
-              x[j] = fmaf(y.x, other, x[j]);
-              x[j + 1] = fmaf(y.y, other, x[j + 1]);
-              x[j + 2] = fmaf(y.z, other, x[j + 2]);
-              x[j + 3] = fmaf(y.w, other, x[j + 3]);
-            }
+            for (int j = 0; j < 16; j++)
+              if (fb != 0.f) x[16 * q + j] = fmaf(__uint_as_float(y[j]), fb, x[16 * q + j]);
           }
-          if (whole) {
-            // bf16: 8 pieces of 16 bytes a row; lanes 8 i .. write row 4 k + i
-            uint8_t* mine8 = stage + row * pitch + (pair ? 0 : c * 256);
+        }
+        if (whole) {
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-              uint32_t h[4];
+          for (int e = 0; e < 8; e++) {
+            uint32_t h[4];
 #pragma unroll
-              for (int k = 0; k < 4; k++) h[k] = f == 0.f ? 0u : bf16x2_of(x[8 * e + 2 * k] * f, x[8 * e + 2 * k + 1] * f);
-              *reinterpret_cast<uint4*>(mine8 + ((e ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
+            for (int k = 0; k < 4; k++) h[k] = bf16x2_of(x[8 * e + 2 * k], x[8 * e + 2 * k + 1]);
+            *reinterpret_cast<uint4*>(mine + ((e ^ (lane & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            const int r = 4 * k + r_in;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
+            const int to = __shfl_sync(~0u, orow, r);
+            if (irow0 + r < rows)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + (size_t)to * D + c * 64 + e_in * 8) = v;
+          }
+          __syncwarp();
+        } else {
+          // fp32: two halves of 32 values
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+              *reinterpret_cast<float4*>(mine + ((e ^ (lane & 7)) << 4)) =
+                  make_float4(x[32 * h + 4 * e], x[32 * h + 4 * e + 1], x[32 * h + 4 * e + 2], x[32 * h + 4 * e + 3]);
             __syncwarp();
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-              const int r = 4 * k + (lane >> 3), e = lane & 7;
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + (wr + r) * pitch + (pair ? 0 : c * 256) +
-                                                              ((e ^ (r & 7)) << 4));
-              const size_t to = __shfl_sync(~0u, (unsigned long long)orow, r);
-              if (__shfl_sync(~0u, (int)valid, r))
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + to * D + c * 64 + e * 8) = v;
+              const int r = 4 * k + r_in;
+              const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
+              if (irow0 + r < rows)
+                *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)(irow0 + r) * D + c * 64 + 32 * h + e_in * 4) = v;
             }
-          } else {
-            // fp32: 64 values a row, in two halves of 8 pieces
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-              uint8_t* mine8 = stage + row * pitch + (pair ? 0 : c * 256);
-#pragma unroll
-              for (int e = 0; e < 8; e++)
-                *reinterpret_cast<float4*>(mine8 + ((e ^ (row & 7)) << 4)) =
-                    make_float4(x[32 * h + 4 * e], x[32 * h + 4 * e + 1], x[32 * h + 4 * e + 2], x[32 * h + 4 * e + 3]);
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 8; k++) {
-                const int r = 4 * k + (lane >> 3), e = lane & 7;
-                const float4 v = *reinterpret_cast<const float4*>(stage + (wr + r) * pitch + (pair ? 0 : c * 256) +
-                                                                  ((e ^ (r & 7)) << 4));
-                if (__shfl_sync(~0u, (int)valid, r))
-                  *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)(irow - lane + r) * D + c * 64 + 32 * h + e * 4) = v;
-              }
-              __syncwarp();
-            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
-      // O is read and the exchange buffer is free before the next item's Q
+      // (single mode: a group's O is read by both)
       tc_fence_before();
       if (!pair) asm volatile("bar.sync 4, 256;" ::: "memory");
       __syncwarp();
