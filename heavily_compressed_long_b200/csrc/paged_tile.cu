@@ -310,41 +310,57 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t rg = 0, u = 0;  // rounds, staging units so far
     // Q rows of an item, bf16, to their places in the Q tiles (rows behind the last: zeros)
     auto load_q = [&](const Item* im) {
-      constexpr int LPR = D / 8;  // 16-byte pieces of a row
-      const int rows = im->rows, n = rows > 128 ? ITEM : 128, w0 = tid - 256, pq = w0 % LPR;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)im->c0 * p.a.q_stride + im->g * p.G * D + pq * 8;
+      constexpr int LPR = D / 8, STEP = 128 / LPR;  // 16-byte pieces of a row, rows a pass (a multiple of 8)
+      const int rows = im->rows, w0 = tid - 256, pq = w0 % LPR, r0 = w0 / LPR;
+      const int qr = im->row0 + r0, qi = p.by_G.div(qr), dq = p.by_G.div(STEP), dh = STEP - dq * p.G;
+      int h = qr - qi * p.G;  // the row's query moves by dq (+ 1), its head by dh (- G)
+      const char* src = static_cast<const char*>(p.a.q) +
+                        2 * ((im->c0 + qi) * p.a.q_stride + (im->g * p.G + h) * D + pq * 8);
+      const int64_t step = 2 * (dq * p.a.q_stride + dh * D), wrap = 2 * (p.a.q_stride - p.G * D);
+      uint32_t dst = smem_u32(sm) + (pq >> 3) * 16384 + r0 * 128 + (((pq & 7) ^ (r0 & 7)) << 4);
+      for (int t = 0; t * 128 < rows; t++, dst += C::QT - 16384) {
 #pragma unroll 4
-      for (int r = w0 / LPR; r < n; r += 128 / LPR) {
-        const int qr = im->row0 + min(r, rows - 1), qi = p.by_G.div(qr);
-        const uint32_t dst = smem_u32(sm) + (r >> 7) * C::QT + (pq >> 3) * 16384 + (r & 127) * 128 + (((pq & 7) ^ (r & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                     "l"(q + qi * p.a.q_stride + (qr - qi * p.G) * D), "r"(r < rows ? 16 : 0)
-                     : "memory");
+        for (int k = 0; k < LPR; k++, dst += STEP * 128) {
+          const bool in = t * 128 + k * STEP + r0 < rows;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(in ? src : p.a.q), "r"(in ? 16 : 0)
+                       : "memory");
+          src += step;
+          h += dh;
+          if (h >= p.G) {
+            h -= p.G;
+            src += wrap;
+          }
+        }
       }
     };
     // this thread's row of Q tile t to fp16 with its exponent taken out
     auto convert_q = [&](int t) {
       const int r = tid - 256;
       uint8_t* qrow = sm + t * C::QT + r * 128;
+      auto at = [&](int e) { return reinterpret_cast<uint4*>(qrow + (e >> 3) * 16384 + (((e & 7) ^ (r & 7)) << 4)); };
       uint32_t top = 0;  // (of magnitudes, whose bits order as their values do; NaN above all)
 #pragma unroll
       for (int e = 0; e < D / 8; e++) {
-        const uint4 x = *reinterpret_cast<const uint4*>(qrow + (e >> 3) * 16384 + (((e & 7) ^ (r & 7)) << 4));
+        const uint4 x = *at(e);
         top = __vmaxu2(__vmaxu2(top, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
                        __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
       }
       float back;
       const float f = row_factor(__uint_as_float(max(top & 0xFFFFu, top >> 16) << 16), &back);
       reinterpret_cast<float*>(sm + C::BACK)[t * 128 + r] = back;
-#pragma unroll 4
-      for (int e = 0; e < D / 8; e++) {
-        uint4* at = reinterpret_cast<uint4*>(qrow + (e >> 3) * 16384 + (((e & 7) ^ (r & 7)) << 4));
-        const uint4 x = *at;
-        uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+      for (int e = 0; e < D / 8; e += 4) {
+        uint4 x[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-          a[k] = half2_of(__uint_as_float(a[k] << 16) * f, __uint_as_float(a[k] & 0xFFFF0000u) * f);
-        *at = make_uint4(a[0], a[1], a[2], a[3]);
+        for (int u = 0; u < 4; u++) x[u] = *at(e + u);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          uint32_t a[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+          for (int k = 0; k < 4; k++)
+            a[k] = half2_of(__uint_as_float(a[k] << 16) * f, __uint_as_float(a[k] & 0xFFFF0000u) * f);
+          *at(e + u) = make_uint4(a[0], a[1], a[2], a[3]);
+        }
       }
     };
     // one staging unit into `tile`
@@ -419,6 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (i == 0) {  // (all four warps come here, whatever their waits said)
           asm volatile("cp.async.wait_all;" ::: "memory");
           asm volatile("bar.sync 5, 128;" ::: "memory");
+#pragma unroll 1
           for (int t = 0; t < qtiles; t++) convert_q(t);
           fence_proxy_async_smem();
           mbar_arrive(q_full);
@@ -733,7 +750,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
           }
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; c++) {
             uint32_t r[32];
 #pragma unroll
@@ -827,69 +844,68 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else if (pair || t == 0) {
         *reinterpret_cast<float4*>(pp + irow * 4) = make_float4(m, M, l, 0.f);
       }
-      // 64 dimensions at a time, through shared memory, so that the warp writes whole rows: lanes
-      // 8 i .. 8 i + 7 write the 8 pieces of 16 bytes of row 4 k + i
+      // 32 dimensions at a time, through shared memory, so that the warp writes whole pieces of rows.
+      // (Loops that are not unrolled: this code runs once an item, and its fetch would take longer.)
       uint8_t* stage = sm + C::OUT + warp * 4096;
       uint8_t* mine = stage + lane * 128;
       const int r_in = lane >> 3, e_in = lane & 7, irow0 = irow - lane;
+      const uint32_t o_at = pair ? tO : tO - t * 128;
+      const int c_lo = pair ? 0 : t * 64, c_hi = pair ? D : min(D, t * 64 + 64);
 #pragma unroll 1
-      for (int c = pair ? 0 : t; c < (pair ? D / 64 : min(t + 1, D / 64)); c++) {
-        float x[64];
-        const uint32_t at = (pair ? tO : tO - t * 128) + 64 * c;
+      for (int c = c_lo; c < c_hi; c += 32) {
+        float x[32];
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-          tmem_ld16(at + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(&x[16 * q])));
+        for (int q = 0; q < 2; q++)
+          tmem_ld16(o_at + c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(reinterpret_cast<uint32_t*>(&x[16 * q])));
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 64; j++) x[j] = fa == 0.f ? 0.f : x[j] * fa;
+        for (int j = 0; j < 32; j++) x[j] = fa == 0.f ? 0.f : x[j] * fa;
         if (!pair) {
+          uint32_t y[32];
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            uint32_t y[16];
-            tmem_ld16(at + 128 + 16 * q, y);
-            tmem_ld_wait();
+          for (int q = 0; q < 2; q++) tmem_ld16(o_at + 128 + c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&y[16 * q]));
+          tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; j++)
-              if (fb != 0.f) x[16 * q + j] = fmaf(__uint_as_float(y[j]), fb, x[16 * q + j]);
-          }
+          for (int j = 0; j < 32; j++)
+            if (fb != 0.f) x[j] = fmaf(__uint_as_float(y[j]), fb, x[j]);
         }
         if (whole) {
+          // bf16, 64 dimensions in the rows' 128 bytes: 8 pieces, four of them now
+          const int half = (c >> 3) & 4;
 #pragma unroll
-          for (int e = 0; e < 8; e++) {
+          for (int e = 0; e < 4; e++) {
             uint32_t h[4];
 #pragma unroll
             for (int k = 0; k < 4; k++) h[k] = bf16x2_of(x[8 * e + 2 * k], x[8 * e + 2 * k + 1]);
-            *reinterpret_cast<uint4*>(mine + ((e ^ (lane & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(mine + (((half + e) ^ (lane & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
           }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; k++) {
-            const int r = 4 * k + r_in;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
-            const int to = __shfl_sync(~0u, orow, r);
-            if (irow0 + r < rows)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + (size_t)to * D + c * 64 + e_in * 8) = v;
-          }
-          __syncwarp();
-        } else {
-          // fp32: two halves of 32 values
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-              *reinterpret_cast<float4*>(mine + ((e ^ (lane & 7)) << 4)) =
-                  make_float4(x[32 * h + 4 * e], x[32 * h + 4 * e + 1], x[32 * h + 4 * e + 2], x[32 * h + 4 * e + 3]);
+          if (half) {
             __syncwarp();
-#pragma unroll
+#pragma unroll 2
             for (int k = 0; k < 8; k++) {
               const int r = 4 * k + r_in;
-              const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
+              const int to = __shfl_sync(~0u, orow, r);
               if (irow0 + r < rows)
-                *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)(irow0 + r) * D + c * 64 + 32 * h + e_in * 4) = v;
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + (size_t)to * D + c - 32 + e_in * 8) = v;
             }
-            __syncwarp();
+          }
+        } else {
+          // fp32
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            *reinterpret_cast<float4*>(mine + ((e ^ (lane & 7)) << 4)) =
+                make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          __syncwarp();
+#pragma unroll 2
+          for (int k = 0; k < 8; k++) {
+            const int r = 4 * k + r_in;
+            const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
+            if (irow0 + r < rows)
+              *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)(irow0 + r) * D + c + e_in * 4) = v;
           }
         }
+        __syncwarp();
       }
       // (single mode: a group's O is read by both)
       tc_fence_before();
