@@ -172,7 +172,7 @@ hcl_status_t launch_paged_attn(const PagedAttnArgs& a, void* ws, cudaStream_t st
     if (e != HCL_OK) return e;
     at += split_workspace(std::min(1024, ROWS_BLOCKS_MOST * num_sms()), ROWS_SMALL, a.kv.d);
   }
-  if ((long long)std::min(a.max_q, a.T) * p.G <= ROWS_SMALL) return HCL_OK;
+  if ((long long)std::max(1, std::min(a.max_q, a.T)) * p.G <= ROWS_SMALL) return HCL_OK;
   p.n_blocks = tile_blocks();
   p.meta = reinterpret_cast<Meta*>(at);
   p.part = reinterpret_cast<float*>(at + meta_bytes(p.n_blocks));

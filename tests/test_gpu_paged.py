@@ -488,6 +488,18 @@ def test_attn_more_queries_than_max_q(hcl):
     assert st.item() == 16 and bool((out[:5] == 3.0).all()) and not bool((out[5] == 3.0).all())
 
 
+@pytest.mark.parametrize("H", [8, 32])
+def test_attn_max_q_of_zero(hcl, H):
+    """No request may have a query then: one that has gets no output, and the status word says so."""
+    gen = torch.Generator().manual_seed(6)
+    table, k, ks, v, vs = make_cache([64, 64], 16, 1, 64, True, gen)
+    q = torch.randn(1, H, 64, generator=gen).to(torch.bfloat16).cuda()
+    out, st = torch.full((1, H, 64), 3.0, dtype=torch.bfloat16, device=DEV), status()
+    hcl.hcl_paged_attn(q, i32([0, 1, 1]), i32([63, 63]), hcl.PagedKV(k.cuda(), ks.cuda()), i32(table), i32([64, 64]),
+                       out, max_q=0, status=st)
+    assert st.item() == 16 and bool((out == 3.0).all())
+
+
 @pytest.mark.parametrize("G,d,lens,news,shared", [(8, 128, [9000, 20000, 100], [1, 1, 1], False),
                                                   (128, 128, [9000, 5000], [1, 1], True),
                                                   (4, 64, [20000], [1], False)])
