@@ -1,12 +1,14 @@
 // paged_rows.cu -- paged attention for requests with few query rows (queries x heads of one KV
 // head <= 16): decode and short drafts.  One pass over the codes, bound by HBM.
 //
-// Block: one producer warp and four consumer warps; two or three blocks per SM.  A unit is 64 KV rows of one request and KV head.  The
-// producer copies its codes with TMA (one box per page, or per 64 rows of a longer page) into a
-// ring of swizzled stages and its page scales with 4-byte asynchronous copies that complete on
-// the same mbarrier; page ids are read eight units at a time, eight ahead.  With at most 8 query
-// rows consumer warps 0, 1 take the even units and 2, 3 the odd ones, each 32 rows; with 9 to 16
-// every unit goes to all four, warps 0, 1 with the first 8 query rows and 2, 3 with the others.
+// Block: one producer warp and four consumer warps; two or three blocks per SM.  A unit is 64 KV
+// rows of one request and KV head.  The producer copies its codes with TMA (one box per page, or
+// per 64 rows of a longer page) into a ring of swizzled stages and its page scales with 4-byte
+// asynchronous copies that complete on the same mbarrier; page ids are read eight units at a time,
+// eight ahead.  With at most 8 query rows consumer warps 0, 1 take the even units and 2, 3 the odd
+// ones, each 32 rows; with 9 to 16 every unit goes to all four, warps 0, 1 with the first 8 query
+// rows and 2, 3 with the others (decode over 64 entries, 16 heads: 13 us with each half on a unit
+// of its own, 10.9 so).
 // Each has its own running softmax, so warps never wait for one another inside an item:
 //   S^T (16 KV rows x 8 query rows) by m16n8k16 fp16 MMAs: KV rows are the M of the MMA, so up to
 //   8 query rows (a group of 8 heads) waste none of it.  The K fragments come from ldmatrix on
@@ -17,7 +19,7 @@
 //   (movmatrix).
 // The bytes bound the kernel once the chain from load to store is covered.  32 requests of up to
 // 32 K rows, 8 KV heads of 8 query heads (1.37 GB, 209 us at the copy rate): 300 us with query
-// rows as M, 16 KV rows a warp and step; 265 us with 32 KV rows; 214 us in this form.
+// rows as M, 16 KV rows a warp and step; 265 us with 32 KV rows; 218 us in this form.
 #include <algorithm>
 
 #include "paged_common.cuh"

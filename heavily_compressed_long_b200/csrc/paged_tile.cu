@@ -3,12 +3,12 @@
 //
 // One persistent block per SM.  An item is 256 query rows (two tiles of 128, the M of an MMA) of
 // one request and KV head; a round is 64 KV rows.  Roles:
-//   warps 0-3 / 4-7   softmax of tile 0 / 1: one thread per query row; they also load Q and
-//                     write the output
+//   warps 0-3 / 4-7   softmax of tile 0 / 1: one thread per query row; they also write the output
 //   warps 12, 15      issue the MMAs of tile 0, 1.  (The tensor pipe takes hardly more than the
 //                     MMA it works on, so what one issuer spends on its barriers must pass under
 //                     the other's MMAs.)  Each tile has two score buffers: S(r+1) is
-//                     issued before PV(r), so a softmax group finds its next scores ready and
+//                     issued before PV(r), the first of an item before the item ahead has written
+//                     its output, so a softmax group finds its next scores ready and
 //                     waits for MMAs only where O has to be rescaled.  (With one buffer and
 //                     rounds of 128, the chain softmax -> PV -> S -> softmax took 6100 clocks a
 //                     round of which the tensor cores worked 2050.)
@@ -19,15 +19,25 @@
 //                     The same layout serves K (K-major B operand of S = Q K^T) and V (MN-major
 //                     B operand of O += P V); rows that are both key and value are widened once.
 //                     (Loading the codes straight into the widening threads' registers spent
-//                     more issue slots on addresses than on the conversion.)
+//                     more issue slots on addresses than on the conversion.)  They also bring an
+//                     item's Q, under the last rounds of the item before it.  (By the softmax
+//                     groups, between two items: 5000 to 8000 clocks in which no MMA ran.)
 // P (fp16) is written over the first half of its S in tensor memory and read there as the A
 // operand.  TMEM: S_0 / P_0 and S_1 / P_1 (two buffers of 64 columns each), O_0, O_1.
 // An item of at most 128 rows (decode over many heads, a request's last rows) runs in single
 // mode: both softmax groups work on the same rows, group t on the rounds of parity t with its
-// own O, and join at the end, so the pipeline keeps its two streams.
+// own O, and join at the end, each reading both O's, so the pipeline keeps its two streams.
 //
-// Bound by the MMA rate and, equally, the exponentials (256 x 64 a round at 16 a clock take as
-// long as the round's MMAs); decode over many heads by the latency of each round's softmax.
+// Bound by the latency of a round's softmax: a warp takes 2400 clocks for its 64 columns (340 to
+// find the scores, 500 to load them, 550 for the maximum, 850 to 1250 for the exponentials, the
+// more where both groups' fall together), with 1300 of MMAs and 1024 of exponentials (256 x 64 at
+// 16 a clock) under it.  Measured and left: exponentials against the old reference while the
+// maximum is formed (chunk of 2048 on 65536: 1151 -> 1136 us, but prompts 589 -> 613), turns
+// between the groups (prompts 589 -> 710), four tiles of each ring fewer or two staging units (the
+// same within 1 %).  Code that runs once an item is kept in loops: unrolled it waited for
+// instructions (prompts 622 -> 588 us).
+//   decode, 8 x 128 K rows x 128 heads on one KV head: 75 us (27 at the MMA rate)
+//   chunk of 2048 x 16 heads on 65536 rows: 1151 us (653);  prompts, 4 x 4096 x 32 heads: 589 us (206)
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -39,8 +49,9 @@ namespace {
 constexpr int TILE = 64;       // KV rows per round
 constexpr int ITEM = ROWS_ITEM;  // query rows per item
 constexpr int THREADS = 16 * 32;
-// What an item costs beyond its rounds (Q, pipeline fill, output), in rounds: the blocks' shares
-// count it, or those of a prompt's first tiles (few rounds, many items) take twice as long.
+// What an item costs beyond its rounds (pipeline fill, output), in rounds: the blocks' shares count
+// it, or those of a prompt's first tiles (few rounds, many items) take twice as long.  (Prompts of
+// 4 x 4096 x 32 heads: 624 us with 5, 592 with 8, 584 with 13; chunks in a window of 128: the same.)
 constexpr int ITEM_COST = 13;
 constexpr int PRING = 16;      // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
