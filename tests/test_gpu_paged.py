@@ -488,6 +488,69 @@ def test_attn_more_queries_than_max_q(hcl):
     assert st.item() == 16 and bool((out[:5] == 3.0).all()) and not bool((out[5] == 3.0).all())
 
 
+@pytest.mark.parametrize("G,news", [(8, [1, 1, 1]), (8, [40, 1, 60]), (32, [1, 2, 1])])
+def test_attn_requests_share_pages(hcl, G, news):
+    """A prefix that three requests have in common stands once, and a page may stand twice in a row."""
+    def poison(table, k, ks, v, vs, q):
+        table[1:, :5] = table[0, :5]
+        table[2, 6] = table[2, 5]
+
+    got = check_attn(hcl, dict(lens=[200, 150, 130], news=news, Hkv=2, G=G, d=64, page=16), poison=poison)
+    assert_attn(*got)
+
+
+@pytest.mark.parametrize("H", [8, 64])
+def test_attn_sixteen_million_rows(hcl, H):
+    """One page that stands 2^18 times in a request's table: out as over the page alone, the
+    log-sum-exp larger by log 2^18.  Beside the usual tolerance, the sums over many rounds: a block has
+    at most 2^18 / 148 rounds on 148 SMs, in two streams of four (row kernel: fewer) additions each,
+    and an addition that truncates loses less than 2^-23 of the sum."""
+    gen = torch.Generator().manual_seed(9)
+    page, d, n = 64, 128, 1 << 18
+    codes = torch.randn(1, 1, page, d, generator=gen).mul(100).to(torch.float8_e4m3fn).view(torch.uint8)
+    ks = torch.full((1, 1), 2.0 ** -6)
+    q = torch.randn(1, H, d, generator=gen).to(torch.bfloat16)
+    out, lse, st = torch.empty(1, H, d, dtype=torch.bfloat16, device=DEV), torch.empty(1, H, device=DEV), status()
+    hcl.hcl_paged_attn(q.cuda(), i32([0, 1]), i32([n * page - 1]), hcl.PagedKV(codes.cuda(), ks.cuda()),
+                       torch.zeros(1, n, dtype=torch.int32, device=DEV), i32([n * page]), out, lse=lse, status=st)
+    assert st.item() == 0
+    want, wl, mass, zabs = ref.attn(ref.f64(q), [0, 1], [page - 1], [page], np.zeros((1, 1), int), codes.numpy(),
+                                    ks.numpy(), None, None, page, 1, 0, 1 / math.sqrt(d))
+    wl = wl + math.log(n)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    long = 4 * (n / sms / 2 + 1) * 2.0 ** -23
+    assert np.all(np.abs(ref.f64(out) - want) <= tolerance(want, mass, zabs) + 2 * long * mass)
+    assert np.all(np.abs(ref.f64(lse) - wl) <= 2.0 ** -16 * zabs + 2.0 ** -19 * (1 + np.abs(wl)) + 2 * long)
+
+
+def test_attn_two_calls_at_once(hcl):
+    """Calls on two streams, each with its own workspace, give what each gives alone."""
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    calls = []
+    for lens, news, G, d in (([4000, 70, 900], [300, 1, 64], 8, 128), ([3000, 2500, 10], [1, 1, 1], 64, 64),
+                             ([9000, 30, 700], [1, 1, 1], 8, 128)):
+        per = -(-max(lens) // 32)
+        k = (torch.randn(3 * per, 2, 32, d, generator=gen, device=DEV) * 100).to(torch.float8_e4m3fn).view(torch.uint8)
+        store = hcl.PagedKV(k, torch.full((3 * per, 2), 2.0 ** -6, device=DEV))
+        table = torch.randperm(3 * per, generator=gen, device=DEV).to(torch.int32).view(3, per)
+        q = torch.randn(sum(news), 2 * G, d, generator=gen, device=DEV).to(torch.bfloat16)
+        ws = torch.empty(hcl.paged_attn_workspace_bytes(sum(news), 2 * G, 2, d), dtype=torch.uint8, device=DEV)
+        args = (q, i32(np.concatenate([[0], np.cumsum(news)])), i32([a - b for a, b in zip(lens, news)]), store, table,
+                i32(lens))
+        out = torch.empty_like(q)
+        calls.append((args, ws, max(news), out, torch.cuda.Stream()))
+    want = []
+    for args, ws, mq, out, _ in calls:
+        want.append(hcl.hcl_paged_attn(*args, torch.empty_like(out), max_q=mq, ws=ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, ws, mq, out, stream in calls:
+            hcl.hcl_paged_attn(*args, out, max_q=mq, ws=ws, stream=stream)
+    torch.cuda.synchronize()
+    for (_, _, _, out, _), w in zip(calls, want):
+        assert torch.equal(out.view(torch.int16), w.view(torch.int16))  # (bits: some codes are NaN)
+
+
 @pytest.mark.parametrize("H", [8, 32])
 def test_attn_max_q_of_zero(hcl, H):
     """No request may have a query then: one that has gets no output, and the status word says so."""
