@@ -37,7 +37,7 @@
 // same within 1 %).  Code that runs once an item is kept in loops: unrolled it waited for
 // instructions (prompts 622 -> 588 us).
 //   decode, 8 x 128 K rows x 128 heads on one KV head: 75 us (27 at the MMA rate)
-//   chunk of 2048 x 16 heads on 65536 rows: 1151 us (653);  prompts, 4 x 4096 x 32 heads: 589 us (206)
+//   chunk of 2048 x 16 heads on 65536 rows: 1148 us (653);  prompts, 4 x 4096 x 32 heads: 579 us (206)
 #include <algorithm>
 
 #include "paged_common.cuh"
@@ -51,8 +51,9 @@ constexpr int ITEM = ROWS_ITEM;  // query rows per item
 constexpr int THREADS = 16 * 32;
 // What an item costs beyond its rounds (pipeline fill, output), in rounds: the blocks' shares count
 // it, or those of a prompt's first tiles (few rounds, many items) take twice as long.  (Prompts of
-// 4 x 4096 x 32 heads: 624 us with 5, 592 with 8, 584 with 13; chunks in a window of 128: the same.)
-constexpr int ITEM_COST = 13;
+// 4 x 4096 x 32 heads: 624 us with 5, 592 with 8, 579 with 11, 585 with 13, 642 with 16; chunks in a
+// window of 128: 53 us with all of them.)
+constexpr int ITEM_COST = 11;
 constexpr int PRING = 16;      // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
