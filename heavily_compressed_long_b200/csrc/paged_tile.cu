@@ -33,9 +33,9 @@
 // more where both groups' fall together), with 1300 of MMAs and 1024 of exponentials (256 x 64 at
 // 16 a clock) under it.  Measured and left: exponentials against the old reference while the
 // maximum is formed (chunk of 2048 on 65536: 1151 -> 1136 us, but prompts 589 -> 613), turns
-// between the groups (prompts 589 -> 710), four tiles of each ring fewer or two staging units (the
-// same within 1 %).  Code that runs once an item is kept in loops: unrolled it waited for
-// instructions (prompts 622 -> 588 us).
+// between the groups (prompts 589 -> 710), scores read twice in rolled halves (chunk 1285), rings
+// of 4 or 2 tiles, two or four staging units (the same within 1 %).  Code that runs once an item
+// is kept in loops: unrolled it waited for instructions (prompts 622 -> 588 us).
 //   decode, 8 x 128 K rows x 128 heads on one KV head: 75 us (27 at the MMA rate)
 //   chunk of 2048 x 16 heads on 65536 rows: 1148 us (653);  prompts, 4 x 4096 x 32 heads: 579 us (206)
 #include <algorithm>
