@@ -95,29 +95,29 @@ __global__ void cp_own_kernel(const int32_t* __restrict__ pos, const int32_t* __
 
 // One warp per (row = sequence x head): G partials o [G, rows, d] bf16, lse [G, rows] fp32
 // (natural log) -> out [rows, d] bf16, lse_out [rows].
-__global__ void lse_merge_kernel(const __nv_bfloat16* __restrict__ o, const float* __restrict__ lse,
-                                 int G, long long rows, int d, int H, const float* __restrict__ sink,
-                                 __nv_bfloat16* __restrict__ out, float* __restrict__ lse_out) {
+// A NaN lse (a NaN among the part's queries or rows) has no order: it makes the row NaN.
+__global__ void lse_merge_kernel(const __nv_bfloat16* o, const float* lse, int G, long long rows, int d, int H,
+                                 const float* sink, __nv_bfloat16* out, float* lse_out) {
   pdl_enter();
   const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (r >= rows) return;
   float M = -INFINITY;
-  for (int g = 0; g < G; g++) M = fmaxf(M, lse[g * rows + r]);
+  for (int g = 0; g < G; g++) M = fmaxf(M, lse[g * rows + r]);  // (fmaxf passes NaN over)
   const float s = sink ? sink[r % H] : -INFINITY;
   M = fmaxf(M, s);
   float den = 0.f;
   for (int g = 0; g < G; g++) {
     const float l = lse[g * rows + r];
-    if (l > -INFINITY) den += __expf(l - M);
+    if (l != -INFINITY) den += __expf(l - M);
   }
-  if (s > -INFINITY) den += __expf(s - M);
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  if (s != -INFINITY) den += __expf(s - M);
+  const float inv = den == 0.f ? 0.f : 1.f / den;  // (0: no part and no sink)
   for (int c = lane * 2; c < d; c += 64) {
     float a0 = 0.f, a1 = 0.f;
     for (int g = 0; g < G; g++) {
       const float l = lse[g * rows + r];
-      if (!(l > -INFINITY)) continue;
+      if (l == -INFINITY) continue;
       const float wgt = __expf(l - M);
       const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(o + ((size_t)g * rows + r) * d + c);
       a0 = fmaf(wgt, __bfloat162float(v.x), a0);
@@ -125,7 +125,7 @@ __global__ void lse_merge_kernel(const __nv_bfloat16* __restrict__ o, const floa
     }
     *reinterpret_cast<__nv_bfloat162*>(out + (size_t)r * d + c) = __floats2bfloat162_rn(a0 * inv, a1 * inv);
   }
-  if (lane == 0 && lse_out) lse_out[r] = den > 0.f ? M + logf(den) : -INFINITY;
+  if (lane == 0 && lse_out) lse_out[r] = den == 0.f ? -INFINITY : M + logf(den);
 }
 
 }  // namespace

@@ -314,7 +314,8 @@ HCL_API hcl_status_t hcl_cache_append(const void* kv_new, const void* gate_new,
  *     lse_parts fp32 [G, rows] (natural log; rows = B * Tq * H, head h = row % H) ->
  *     out bf16 [rows, d] = sum_r w_r o_r / sum_r w_r with w_r = exp(lse_r - M), and lse_out
  *     fp32 [rows] (or NULL) = M + log sum_r w_r, M the largest lse; a sink (fp32 [H] logits or
- *     NULL) adds exp(sink[h] - M) to the denominator only.  Partials with lse = -inf weigh 0.
+ *     NULL) adds exp(sink[h] - M) to the denominator only.  Partials with lse = -inf weigh 0,
+ *     whatever they hold; a NaN lse makes its row of out and lse_out NaN.
  */
 HCL_API hcl_status_t hcl_cp_candidates(const void* scores, int score_fmt, const int32_t* idx, int B,
                                        int Nc_local, int k, int e0, float* cand_scores,

@@ -1,0 +1,96 @@
+"""The layers over paged 8-bit caches, the merge of their parts, and the page plan's sizes."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_ref as ref
+from tests.test_gpu_paged import PlanState, i32, status
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+# ------------------------------------------------------------------------------------ merge
+
+
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("G,part", [(1, 0), (2, 0), (2, 1), (3, 1)])
+def test_merge_keeps_nan(hcl, G, part, sink):
+    """A part whose log-sum-exp is NaN makes its row NaN, and no other row; a part that weighs
+    nothing may hold anything."""
+    gen = torch.Generator().manual_seed(G + part)
+    rows, H, d = 8, 4, 64
+    o = torch.randn(G, rows, d, generator=gen).to(torch.bfloat16)
+    lse = torch.randn(G, rows, generator=gen)
+    lse[part, 2] = math.nan
+    lse[part, 5] = -math.inf
+    o[part, 5] = math.nan
+    s = torch.randn(H, generator=gen) if sink else None
+    out = torch.zeros(rows, d, dtype=torch.bfloat16, device=DEV)
+    got_l = torch.zeros(rows, device=DEV)
+    hcl.hcl_lse_merge(o.view(G, 2, H, d).cuda(), lse.view(G, 2, H).cuda(), out.view(2, H, d),
+                      lse_out=got_l.view(2, H), sink=None if s is None else s.cuda())
+    z = lse.double()
+    if sink:
+        z = torch.cat([z, s.double().repeat(rows // H)[None]])
+    want_l = torch.logsumexp(z, 0)
+    w = torch.exp(lse.double() - torch.where(torch.isneginf(want_l), 0.0, want_l))
+    want = (torch.where(w[..., None] == 0, 0.0, o.double()) * w[..., None]).sum(0)
+    nan = torch.arange(rows) == 2
+    assert torch.isnan(out.cpu()[nan]).all() and torch.isnan(got_l.cpu()[nan]).all()
+    assert not torch.isnan(out.cpu()[~nan]).any()
+    # bf16: half a step; weights by exponentials of differences below 8, a few steps of 2^-24 each
+    err = (out.cpu().double() - want).abs()[~nan]
+    assert bool((err <= 2.0 ** -8 * want.abs()[~nan] + 2.0 ** -18 * (w[..., None] * o.double().abs().nan_to_num()).sum(0)[~nan]).all())
+    fin = ~nan & torch.isfinite(want_l)
+    assert torch.equal(torch.isneginf(got_l.cpu()[~nan]), torch.isneginf(want_l[~nan]))
+    assert bool(((got_l.cpu().double() - want_l).abs()[fin] <= 2.0 ** -20 * (1 + want_l.abs()[fin])).all())
+
+
+def hca_layer(H, T, entries_T, n_entries, gen, sink=None, raw_rows=200):
+    """A PagedHcaLayer of one request with raw rows and entries in its caches; the plan of the step
+    covers the last T rows."""
+    from heavily_compressed_long_b200.pipeline import PagedBatch, PagedHcaLayer
+    d, mh = 128, 16
+    raw, ent = PagedBatch(1, 16, 20, 24, T), PagedBatch(1, 16, 2, 4, entries_T)
+    layer = PagedHcaLayer(raw, ent, 24, 4, H, d, mh=mh, W=64, sink=sink)
+    at = 0
+    while at < raw_rows:
+        n = min(T, raw_rows - at)
+        raw.plan(i32([n]))
+        layer.raw_layer.write(torch.randn(T, 1, d, generator=gen).to(torch.bfloat16).cuda())
+        at += n
+    for _ in range(n_entries // entries_T):
+        ent.plan(i32([entries_T]))
+        layer.entry_layer.write(torch.randn(entries_T, 1, d, generator=gen).to(torch.bfloat16).cuda())
+    return layer, raw, ent
+
+
+@pytest.mark.parametrize("with_sink", [False, True])
+@pytest.mark.parametrize("where", ["query", "entry", "raw"])
+def test_hca_layer_keeps_nan(hcl, where, with_sink):
+    """A NaN in a query, or in an entry or a raw row that the queries see, comes out as NaN."""
+    gen = torch.Generator().manual_seed(3)
+    H, T = 16, 4
+    sink = torch.randn(H, generator=gen).cuda() if with_sink else None
+    layer, raw, ent = hca_layer(H, T, 4, 8, gen, sink=sink)
+    q = torch.randn(T, H, 128, generator=gen).to(torch.bfloat16)
+    rows, heads = slice(None), slice(None)
+    if where == "query":
+        q[1, 3, 7] = math.nan
+        rows, heads = slice(1, 2), slice(3, 4)
+    elif where == "entry":
+        layer.entry_layer.store.k[ent.table[0, 0].item(), 0, 5, 11] = 0x7F
+    else:
+        layer.raw_layer.store.k[raw.table[0, 190 // 16].item(), 0, 190 % 16, 11] = 0x7F
+    out = torch.zeros(T, H, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros(T, H, device=DEV)
+    layer.attend(q.cuda(), out, lse=lse, max_q=T)
+    assert raw.status.item() == 0 and ent.status.item() == 0
+    want = torch.zeros(T, H, dtype=torch.bool)
+    want[rows, heads] = True
+    assert torch.equal(torch.isnan(lse).cpu(), want)
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
