@@ -22,6 +22,7 @@ namespace {
 // updated in place and a captured launch can be replayed.  Latency bound.
 
 constexpr int PP_THREADS = 1024;
+constexpr int PP_STATIC = 1024;  // its static shared memory takes less than this
 constexpr int PP_SAT = (1 << 30) - 1;  // row counts saturate here (T <= 2^29)
 
 struct PlanSum {
@@ -50,6 +51,7 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
   int* s_need = s_back + p.B + 1;    // [B + 1] of the taken pages
   __shared__ PlanSum s_warp[32];
   __shared__ int s_used;
+  static_assert(sizeof(s_warp) + sizeof(s_used) <= PP_STATIC / 2, "PP_STATIC");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
   const int gid = blockIdx.x * nthr + tid, gsize = gridDim.x * nthr;
   const int pmask = p.page - 1;
@@ -355,7 +357,8 @@ int log2_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 
 
 hcl_status_t launch_page_plan(const PagePlanArgs& a, cudaStream_t st) {
   const int smem = (4 * a.B + 3) * 4;
-  if (smem > 48 * 1024) {
+  // (the 48 KB that a launch may have without asking count the kernel's static arrays too)
+  if (smem > 48 * 1024 - PP_STATIC) {
     hcl_status_t e = set_kernel_attrs(reinterpret_cast<const void*>(page_plan_kernel), smem, false);
     if (e != HCL_OK) return e;
   }

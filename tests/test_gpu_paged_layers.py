@@ -1,5 +1,8 @@
 """The layers over paged 8-bit caches, the merge of their parts, and the page plan's sizes."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,28 @@ from tests.test_gpu_paged import PlanState, i32, status
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+
+
+# ------------------------------------------------------------------------------------ plan
+
+
+@pytest.mark.parametrize("B", [3040, 3046, 3047, 3060, 3071, 3072, 8192])
+def test_plan_many_requests(hcl, B):
+    """Numbers of requests around the shared memory that a launch has without asking, and the most."""
+    rng = np.random.default_rng(B)
+    S = PlanState(B, 3, 2 * B, 16, 3 * B, rng)
+    S.step(hcl, [0] * B, rng.integers(0, 4, B).tolist())
+    S.step(hcl, [max(0, n - 1) for n in S.seq], rng.integers(0, 3, B).tolist())
+
+
+def test_plan_many_requests_first_in_a_process(hcl):
+    """The same where no larger call has gone before it in the process."""
+    code = ("import numpy as np; from heavily_compressed_long_b200 import api; "
+            "from tests.test_gpu_paged import PlanState; rng = np.random.default_rng(0); "
+            "PlanState(3060, 2, 4000, 16, 9000, rng).step(api, [0] * 3060, rng.integers(0, 3, 3060).tolist())")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------------------------ merge
