@@ -210,13 +210,15 @@ class PagedAttnLayer:
     """One attention layer over a paged 8-bit cache: the step's new rows are written, then its
     queries attend (causal; with W only over the last W rows; with m over entries of m tokens).
 
-    shared: rows are both key and value (H query heads on Hkv of them)."""
+    shared: rows are both key and value (H query heads on Hkv of them).  max_T: the most query rows
+    of a call (default: the batch's T).  The workspace is the layer's: two calls of attend on one
+    layer must not overlap."""
 
     def __init__(self, batch: PagedBatch, n_pages, H, Hkv, d, shared=False, m=1, W=0, sink=None,
-                 device="cuda"):
+                 device="cuda", max_T=None):
         self.batch, self.m, self.W, self.sink, self.H = batch, m, W, sink, H
         self.store = api.PagedKV.empty(n_pages, Hkv, batch.page, d, shared=shared, device=device)
-        n = api.paged_attn_workspace_bytes(batch.T, H, Hkv, d)
+        n = api.paged_attn_workspace_bytes(batch.T if max_T is None else max_T, H, Hkv, d)
         self.ws = torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
     def write(self, k_new, v_new=None, stream=None):
@@ -244,14 +246,16 @@ class PagedHcaLayer:
     log-sum-exp with the sink.  Rows are both key and value, one for all H heads.
 
     raw and entries are PagedBatch's, planned for tokens and for completed entries; the rows of
-    both are written with raw_layer.write and entry_layer.write before attend."""
+    both are written with raw_layer.write and entry_layer.write before attend.  The workspaces and
+    partial results are the layer's: two calls of attend on one layer must not overlap."""
 
     def __init__(self, raw: PagedBatch, entries: PagedBatch, n_raw_pages, n_entry_pages, H, d, mh=128,
                  W=128, sink=None, device="cuda"):
         self.raw, self.entries, self.sink = raw, entries, sink
         self.raw_layer = PagedAttnLayer(raw, n_raw_pages, H, 1, d, shared=True, W=W, device=device)
+        # (its queries are the raw batch's)
         self.entry_layer = PagedAttnLayer(entries, n_entry_pages, H, 1, d, shared=True, m=mh,
-                                          device=device)
+                                          device=device, max_T=raw.T)
         self.o_parts = torch.zeros(2, raw.T, H, d, dtype=torch.bfloat16, device=device)
         self.lse_parts = torch.empty(2, raw.T, H, dtype=torch.float32, device=device)
 

@@ -119,3 +119,24 @@ def test_hca_layer_keeps_nan(hcl, where, with_sink):
     want[rows, heads] = True
     assert torch.equal(torch.isnan(lse).cpu(), want)
     assert torch.equal(torch.isnan(out).all(-1).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
+
+
+@pytest.mark.parametrize("H,T,entries_T", [(16, 4, 1), (8, 8, 2), (64, 3, 1)])
+def test_hca_layer_with_more_queries_than_new_entries(hcl, H, T, entries_T):
+    """The entry batch plans fewer rows a step than the raw batch has queries: the result is that of
+    a layer whose entry batch is as large."""
+    got = []
+    for n in (entries_T, T):
+        gen = torch.Generator().manual_seed(8)
+        layer, raw, ent = hca_layer(H, T, entries_T, 6, gen)
+        if n != entries_T:
+            from heavily_compressed_long_b200.pipeline import PagedBatch, PagedHcaLayer
+            big = PagedBatch(1, 16, 2, 4, T)
+            big.seq_len, big.table = ent.seq_len, ent.table
+            other = PagedHcaLayer(raw, big, 24, 4, H, 128, mh=16, W=64)
+            other.raw_layer.store, other.entry_layer.store = layer.raw_layer.store, layer.entry_layer.store
+            layer = other
+        q = torch.randn(T, H, 128, generator=gen).to(torch.bfloat16).cuda()
+        got.append(layer.attend(q, torch.zeros(T, H, 128, dtype=torch.bfloat16, device=DEV), max_q=T))
+        assert raw.status.item() == 0 and ent.status.item() == 0
+    assert torch.isfinite(got[0]).all() and (got[0] != 0).any() and torch.equal(*got)
