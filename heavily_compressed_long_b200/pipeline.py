@@ -187,7 +187,7 @@ class PagedBatch:
             return torch.full(shape, value, dtype=torch.int32, device=device)
 
         self.B, self.page, self.T = B, page, T
-        self.seq_len, self.start = i32(B), i32(B)
+        self.seq_len, self.start, self._keep, self._zero = i32(B), i32(B), i32(B), i32(1)
         self.table = i32(B, max_pages, value=-1)
         self.free_list = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
         self.n_free = i32(1, value=n_pages)
@@ -198,12 +198,18 @@ class PagedBatch:
         """One step: of each request keep[b] rows stay (default: all; 0 for a new request in the
         row) and new_len[b] rows (int32 [B]) are added.  Afterwards start holds the first new
         row's position, slot and pos the new rows' places (-1 behind the last), seq_len the
-        lengths.  The status word has HCL_ERR_NO_PAGES where a request did not get its rows."""
+        lengths.  The status word has HCL_ERR_NO_PAGES where a request did not get its rows, and
+        HCL_ERR_DEVICE_FAULT where keep was out of range: it counts as the nearest length that the
+        request can keep."""
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            self.start.copy_(self.seq_len if keep is None else keep)
-        api.hcl_page_plan(self.start, new_len, self.seq_len, self.table, self.free_list, self.n_free,
-                          self.page, self.cu_new, self.pos, self.slot, status=self.status,
-                          stream=stream)
+            if keep is None:
+                self.start.copy_(self.seq_len)
+            else:
+                self._keep.copy_(keep)
+                torch.clamp(self._keep, min=self._zero, max=self.seq_len, out=self.start)
+        api.hcl_page_plan(self.start if keep is None else self._keep, new_len, self.seq_len, self.table,
+                          self.free_list, self.n_free, self.page, self.cu_new, self.pos, self.slot,
+                          status=self.status, stream=stream)
 
 
 class PagedAttnLayer:

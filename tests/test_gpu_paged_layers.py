@@ -38,6 +38,21 @@ def test_plan_many_requests_first_in_a_process(hcl):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+def test_batch_start_is_the_first_new_row(hcl):
+    """Also where keep is out of range: the positions that the plan gives, and the start that the
+    attention uses, are the same."""
+    from heavily_compressed_long_b200.pipeline import PagedBatch
+    b = PagedBatch(3, 16, 4, 12, 40)
+    b.plan(i32([20, 5, 9]))
+    b.plan(i32([1, 2, 3]), keep=i32([25, -4, 9]))
+    assert b.status.item() == 16
+    assert b.start.tolist() == [20, 0, 9] and b.seq_len.tolist() == [21, 2, 12]
+    assert b.pos[:6].tolist() == [20, 0, 1, 9, 10, 11]
+    b.status.zero_()
+    b.plan(i32([1, 1, 1]), keep=torch.tensor([21, 1, 0], device=DEV))  # (any integer type)
+    assert b.status.item() == 0 and b.start.tolist() == [21, 1, 0] and b.seq_len.tolist() == [22, 2, 1]
+
+
 # ------------------------------------------------------------------------------------ merge
 
 
