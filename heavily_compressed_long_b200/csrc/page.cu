@@ -110,11 +110,12 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
   __syncthreads();
 
   // releases: the r-th released page goes to place top - 1 - r of the stack
-  for (int r = gid; r < tot.back; r += gsize) {
+  // (r is unsigned: the counts reach 2^31 - 1 where lengths that nothing holds are given back)
+  for (uint32_t r = gid; r < (uint32_t)tot.back; r += gsize) {
     const int b = find_request(s_back, p.B, r);
     const int j = ((s_keep[b] + pmask) >> sh) + (r - s_back[b]);
     const int id = p.table[(size_t)b * p.max_pages + j];
-    if (r < top) p.free_list[top - 1 - r] = id;
+    if (r < (uint32_t)top) p.free_list[top - 1 - r] = id;
     else fault = HCL_ERR_DEVICE_FAULT;
   }
   __syncwarp();
@@ -136,18 +137,18 @@ __global__ void __launch_bounds__(PP_THREADS, 1) page_plan_kernel(PagePlanArgs p
   };
 
   // takes: the r-th taken page is place top - 1 - r of the stack
-  for (int r = gid; r < tot.need; r += gsize) {
+  for (uint32_t r = gid; r < (uint32_t)tot.need; r += gsize) {
     const int b = find_request(s_need, p.B, r);
     if (!admitted(b)) continue;
     const int j = ((s_keep[b] + pmask) >> sh) + (r - s_need[b]);
     p.table[(size_t)b * p.max_pages + j] = p.free_list[top - 1 - r];
   }
   // released entries that are not taken again
-  for (int r = gid; r < tot.back; r += gsize) {
+  for (uint32_t r = gid; r < (uint32_t)tot.back; r += gsize) {
     const int b = find_request(s_back, p.B, r);
     const int kept = (s_keep[b] + pmask) >> sh;
     const int got = admitted(b) ? s_need[b + 1] - s_need[b] : 0;
-    if (r - s_back[b] >= got) p.table[(size_t)b * p.max_pages + kept + (r - s_back[b])] = -1;
+    if ((int)(r - s_back[b]) >= got) p.table[(size_t)b * p.max_pages + kept + (r - s_back[b])] = -1;
   }
   // a slot for every new row
   const int rows = min(s_rows[p.B], p.T);

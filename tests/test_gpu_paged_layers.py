@@ -38,6 +38,18 @@ def test_plan_many_requests_first_in_a_process(hcl):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+def test_plan_gives_back_two_to_the_31_entries(hcl):
+    """The largest table, all of it given back though the cache has four pages: what does not fit
+    the free list is refused, the table is cleared to its end."""
+    B, width = 16, (1 << 27) - 1
+    table = torch.full((B, width), 3, dtype=torch.int32, device=DEV)
+    seq, free, n = i32([width * 16] * B), i32([0, 1, 2, 3]), i32([0])
+    cu, pos, slot, st = i32([0] * (B + 1)), i32([0]), i32([0]), status()
+    hcl.hcl_page_plan(i32([0] * B), i32([0] * B), seq, table, free, n, 16, cu, pos, slot, status=st)
+    assert st.item() == 16 and n.item() == 4 and seq.tolist() == [0] * B and free.tolist() == [3] * 4
+    assert bool((table.view(-1)[:1 << 30] == -1).all()) and bool((table.view(-1)[1 << 30:] == -1).all())
+
+
 def test_batch_start_is_the_first_new_row(hcl):
     """Also where keep is out of range: the positions that the plan gives, and the start that the
     attention uses, are the same."""
