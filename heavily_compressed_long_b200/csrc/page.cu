@@ -232,11 +232,17 @@ __global__ void __launch_bounds__(PW_THREADS) paged_write_kernel(PagedWriteArgs 
     bool begins = false;
     if (tid < chunk && t < t_hi) {
       const int slot = p.slot[t];
-      begins = slot >= 0 && (t == 0 || (slot & (page - 1)) == 0 || p.slot[t - 1] != slot - 1);
+      const int prev = t > 0 ? p.slot[t - 1] : -1;
+      // A row behind another of its page goes on with that run.  Where it is not the next slot it
+      // begins none (two blocks would set the page's scale at once): it is left out.
+      const bool goes_on = slot >= 0 && prev >= 0 && (prev >> sh) == (slot >> sh);
+      begins = slot >= 0 && !goes_on;
+      bool fault = goes_on && slot != prev + 1;
       if (begins && (slot >> sh) >= p.kv.n_pages) {
         begins = false;
-        report(p.status, HCL_ERR_DEVICE_FAULT);
+        fault = true;
       }
+      if (fault) report(p.status, HCL_ERR_DEVICE_FAULT);
     }
     const uint32_t mask = __ballot_sync(~0u, begins);
     if (lane == 0 && warp < 4) s_begin[warp] = mask;

@@ -391,9 +391,11 @@ HCL_API hcl_status_t hcl_page_plan(const int32_t* keep, const int32_t* new_len, 
  * saturating (infinities too); NaN stays NaN.  When the scale grows, the rows before the first
  * new one are rounded again to the new scale (exact but for values that become subnormal); the
  * rows behind the last new one are left as they were.
- * The rows of one page must stand together in slot, in ascending order, each once (as
- * hcl_page_plan writes them); a page that stands in two places is written in no defined order.
- * Slots beyond the cache are skipped: HCL_ERR_DEVICE_FAULT.
+ * The rows of one page must stand together in slot, each behind the one before it in the page (as
+ * hcl_page_plan writes them): slots s, s + 1, ...  A row that follows another of its page without
+ * being the next one, and those that go on from it, are skipped: HCL_ERR_DEVICE_FAULT.  So are
+ * slots beyond the cache.  A page that stands in two places, with other slots between, is written
+ * in no defined order.
  */
 HCL_API hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const void* v_new,
                                      int64_t v_stride, const int32_t* slot, int T,

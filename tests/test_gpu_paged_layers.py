@@ -65,6 +65,35 @@ def test_batch_start_is_the_first_new_row(hcl):
     assert b.status.item() == 0 and b.start.tolist() == [21, 1, 0] and b.seq_len.tolist() == [22, 2, 1]
 
 
+# ------------------------------------------------------------------------------------ write
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("order,written", [((3, 5, 6), 1), ((5, 3), 1), ((4, 4), 1), ((0, 0), 1), ((7, 8, 0, 1), 2),
+                                           ((2, 3, 4, 6, 7), 3)])
+@pytest.mark.parametrize("pad", [0, 200])
+def test_write_rows_of_a_page_not_in_order(hcl, page, order, written, pad):
+    """Rows of one page that are not one run of slots: the first run is written, the others are left
+    out and the status says so; the pages around it are as without them."""
+    gen = torch.Generator().manual_seed(page)
+    n_pages, Hkv, d = 20, 3, 64
+    slot = list(range(5 * page, 5 * page + min(pad, 9 * page)))
+    first = len(slot)
+    slot += [2 * page + o for o in order] + [3 * page, 3 * page + 1]
+    x = (torch.randn(len(slot), Hkv, d, generator=gen) * torch.exp2(torch.randn(len(slot), 1, 1, generator=gen) * 4))
+    x = x.to(torch.bfloat16)
+    codes = (torch.randn(n_pages, Hkv, page, d, generator=gen) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    scale = torch.exp2(torch.randint(-9, 0, (n_pages, Hkv), generator=gen).float())
+    c, s, st = codes.cuda(), scale.cuda(), status()
+    hcl.hcl_paged_write(x.cuda(), None, i32(slot), hcl.PagedKV(c, s), status=st)
+    assert st.item() == 16
+    kept = np.asarray(slot)
+    kept[first + written:first + len(order)] = -1
+    val, want = ref.write(ref.f64(x), kept, codes.numpy(), scale.numpy())
+    np.testing.assert_array_equal(ref.f64(s), want)
+    np.testing.assert_array_equal(ref.decode_e4m3(c.cpu().numpy()), val)
+
+
 # ------------------------------------------------------------------------------------ merge
 
 
