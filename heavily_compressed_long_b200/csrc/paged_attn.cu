@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
       for (int e = 0; e < E; e++) a[e] = 0.f;
 #pragma unroll 4
       for (int k = 0; k < n; k++) add_part<E>(a, part(k) + ROWS * 4 + (size_t)row * D + lane * E, __shfl_sync(~0u, f, k));
-      const float fo = finish_row(m, M, l, sink2, &lse);
+      const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &lse);
 #pragma unroll
       for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t*>(out + lane * E + e) = fo == 0.f ? 0u : bf16x2_of(a[e] * fo, a[e + 1] * fo);
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
 #pragma unroll
     for (int e = 0; e < E; e++) s_o[warp][lane * E + e] = a[e];
     __syncthreads();
-    const float fo = finish_row(m, M, l, sink2, &lse);
+    const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &lse);
     for (int e = tid; e < D; e += MW * 32) {
       float x = 0.f;
 #pragma unroll

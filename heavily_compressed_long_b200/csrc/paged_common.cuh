@@ -10,12 +10,20 @@
 // here); the merge kernel joins them.
 //
 // Numerics.  Codes are exact in fp16 and so is a query row after its exponent is taken out
-// (2^e with the row's largest magnitude in [2^14, 2^15)), so the fp16 products of Q K^T are
-// exact and summed in fp32:  z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
-// A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + 4) with
-// lv = log2(v_scale) and M >= max(z2 + lv) - 11 a running reference, rounded to fp16 (11 bits
-// down to 2^-18 of the largest, nothing below 2^-29), and O = sum P * code in fp32 needs no further scale.
-// The softmax sum is l = sum 2^(z2 - m) with m = M - 4 - lvref, lvref the largest lv met so far:
+// (2^e with the row's largest magnitude in [2^14, 2^15); components below 2^-28 of the largest
+// lose bits, by at most 2^-40 of it), so the fp16 products of Q K^T are exact and summed in fp32:  z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
+// A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + P_OFF)
+// with lv = log2(v_scale) and M >= max(z2 + lv) - (15 - P_OFF) a running reference, rounded to
+// fp16, and O = sum P * code in fp32 needs no further scale.  fp16 holds 11 bits down to 2^-14 and
+// multiples of 2^-24 below: with P_OFF = 15, M the maximum itself, a row's weight keeps 11 bits
+// down to 2^-29 of the largest and is zero below 2^-40 (a row that outweighs all others may have
+// values of zero, so that the others make the output).  The row kernel pays nothing for that (245
+// against 244 us for the grouped decode); where M may lag by 11 the tile kernel rescales O less
+// often, and a reference that lags by up to 3 (2^-26, 2^-37) costs it 0.4 to 2 %.  Measured and
+// left: P as two bf16 parts, which keeps 16 bits at any weight (prompts 579 -> 739 us, chunk of
+// 2048 on 65536 rows 1150 -> 1385); in the row kernel the rows below 2^-14 times 2^28 in MMAs of
+// their own (grouped decode 245 -> 266, drafts 79 -> 88).
+// The softmax sum is l = sum 2^(z2 - m) with m = M - P_OFF - lvref, lvref the largest lv met so far:
 // formed from the unrounded P of each group of 16 rows (never more than one page) times
 // 2^(lvref - lv), and moved when M or lvref grow.  Since M <= max z2 + lvref its largest term is
 // not far below 1.  lv is not taken below lvref - 60 (a page of zeros has the scale 2^-126), and
@@ -33,8 +41,8 @@ namespace paged {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float P_OFF = 4.f;       // P's largest magnitude is 2^P_OFF .. 2^(P_OFF + P_LAZY) <= 2^15
-constexpr float P_LAZY = 11.f;     // M may lag its maximum by this much
+// P's largest magnitude is 2^P_OFF .. 2^15; M may lag its maximum by 15 - P_OFF.
+constexpr float P_OFF_ROWS = 15.f, P_OFF_TILE = 12.f;
 constexpr float LV_SPAN = 60.f;
 constexpr float SCALE_MIN = 1.17549435e-38f;  // 2^-126
 constexpr int ROWS_SMALL = 16;     // query rows (queries x heads of a KV head) of the row kernel
@@ -227,6 +235,15 @@ __device__ __forceinline__ uint32_t half2_of_codes(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+// The same as bf16 (exact).
+__device__ __forceinline__ uint32_t bf2_of_codes(uint16_t c) {
+  const uint32_t h = half2_of_codes(c);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return bf16x2_of(f.x, f.y);
+}
+__device__ __forceinline__ unsigned long long f2_sub(unsigned long long a, unsigned long long b) {
+  return f2_fma(b, f2_make(-1.f, -1.f), a);
+}
 // 0xFF in every byte of x that is a NaN code (0x7F with either sign).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
   return __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
@@ -242,6 +259,7 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
 
 // The final row from O (value units), l and m (log2 units): factor for O and the log-sum-exp.
 // M: O's reference; the sink's logit in log2 units, or -inf.
+template <bool ROWS>
 __device__ __forceinline__ float finish_row(float m, float M, float l, float sink2, float* lse) {
   if (!(l > 0.f) && !(l != l)) {  // no row
     *lse = sink2 == -INFINITY ? -INFINITY : sink2 * LN2;
@@ -250,7 +268,7 @@ __device__ __forceinline__ float finish_row(float m, float M, float l, float sin
   const float mm = fmaxf(m, sink2);
   const float lt = l * exp2f(m - mm) + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - mm));
   *lse = (mm + log2f(lt)) * LN2;
-  return exp2f(M - P_OFF - mm) / lt;
+  return exp2f(M - (ROWS ? P_OFF_ROWS : P_OFF_TILE) - mm) / lt;
 }
 
 // Kernels for requests of up to ROWS_SMALL query rows (`rows`: the most that one of them can

@@ -33,6 +33,7 @@ constexpr int THREADS = (NW + 1) * 32;
 constexpr int TILE = 64;               // KV rows per unit
 constexpr int NG = 2;                  // groups of 16 rows (never more than a page) per warp and unit
 constexpr int WPT = TILE / (16 * NG);  // warps per unit
+constexpr float P_OFF = P_OFF_ROWS, P_LAZY = 15.f - P_OFF;
 
 // Blocks per SM: three where an even number of stages leaves the room.
 constexpr int blocks_per_sm(int d, bool shared) { return d == 128 && !shared ? 2 : 3; }
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
           const int i = p.by_G.div(row), head = w.g * p.G + row - i * p.G;
           const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
           float lse;
-          const float f = finish_row(mt, Mt, lt, p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
+          const float f = finish_row<true>(mt, Mt, lt, p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + col) =
               f == 0.f ? make_uint2(0, 0) : make_uint2(bf16x2_of(a.x * f, a.y * f), bf16x2_of(a.z * f, a.w * f));
           if (col == 0 && p.a.lse) p.a.lse[orow] = lse;

@@ -46,6 +46,7 @@ namespace hcl {
 namespace paged {
 namespace {
 
+constexpr float P_OFF = P_OFF_TILE, P_LAZY = 15.f - P_OFF;
 constexpr int TILE = 64;       // KV rows per round
 constexpr int ITEM = ROWS_ITEM;  // query rows per item
 constexpr int THREADS = 16 * 32;
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float* pp = p.part + (2 * (size_t)blockIdx.x + (im->head ? 0 : 1)) * part_floats(ITEM, D);
       if (whole) {
         float lse;
-        const float f = finish_row(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
+        const float f = finish_row<false>(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
         fa *= f;
         fb *= f;
         if (valid && p.a.lse && (pair || t == 0)) p.a.lse[orow] = lse;

@@ -417,9 +417,11 @@ HCL_API hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const 
  *   chooses the kernels; a request with more gets no output and HCL_ERR_DEVICE_FAULT).
  *   ws: hcl_paged_attn_workspace_bytes() bytes of scratch, its contents unspecified before and
  *   after; two calls that may overlap need one each.
- * Page scales must be positive and finite; those below 2^-126 count as 2^-126.  A row whose
- * softmax weight times its value scale is below 2^-60 of the largest value scale that the query
- * sees may count as zero in out (never in lse).  Pages outside
+ * Page scales must be positive and finite; those below 2^-126 count as 2^-126.  out takes each
+ * row's softmax weight times its value scale in 11 bits, and where that product is below 2^-26 of
+ * the query's largest, in multiples of 2^-36 of the largest (or of 2^-84 of the largest value scale
+ * that the query sees, where that is more): below 2^-37 of the largest a row may count as zero in
+ * out, never in lse.  Pages outside
  * the cache, and rows beyond max_pages * page, are left out: HCL_ERR_DEVICE_FAULT.  Rows at or
  * behind kv_len, and pages that no query of the request sees, are not read into the result,
  * whatever their codes.  A NaN code reaches only queries that see its row: in a key it makes out
