@@ -26,9 +26,11 @@
 // The softmax sum is l = sum 2^(z2 - m) with m = M - P_OFF - lvref, lvref the largest lv met so far:
 // formed from the unrounded P of each group of 16 rows (never more than one page) times
 // 2^(lvref - lv), and moved when M or lvref grow.  Since M <= max z2 + lvref its largest term is
-// not far below 1.  lv is not taken below lvref - 60 (a page of zeros has the scale 2^-126), and
-// where lvref grows so far that l would pass 2^60, M is raised with it: the values of a page
-// whose scale is below 2^-60 of the largest count as zero, its rows' share of the sum does not.
+// not far below 1.  lvref belongs to a query row: a page that the row does not see does not move
+// it.  lv is not taken below lvref - 60 (a page of zeros has the scale 2^-126), and where lvref
+// grows so far that l would pass 2^60, M is raised with it: the values of a page whose scale is
+// below 2^-60 of the largest that the row sees count with 2^-60 of it or less, its rows' share of
+// the sum stays right.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -305,10 +305,11 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
 #pragma unroll
       for (int k = 0; k < 4; k++) o[c][k] = 0.f;
     const int rows0 = (warp % WPT) * 16 * NG;  // this warp's rows of a tile
-    float M[2], l[2], lvref = -INFINITY;
+    float M[2], l[2], lvref[2];
+    bool alike = true;  // lvref is one for all query rows of the warp
 #pragma unroll
     for (int r = 0; r < 2; r++) {
-      M[r] = -INFINITY;
+      M[r] = lvref[r] = -INFINITY;
       l[r] = 0.f;
     }
 
@@ -373,38 +374,27 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
             }
           poison = __reduce_or_sync(~0u, poison);
         }
-        float lv[NG], wl[NG], kc[NG];
-        const float lvold = lvref;
+        float lvg[NG], kc[NG], Mo[2];  // Mo: O's reference
 #pragma unroll
         for (int g = 0; g < NG; g++) {
-          lv[g] = log2_scale(SHARED ? ks[g] : s_scale[st * 8 + 4 + (rows0 >> 4) + g]);
-          if (ks[g] > 0.f) lvref = fmaxf(lvref, lv[g]);
+          lvg[g] = log2_scale(SHARED ? ks[g] : s_scale[st * 8 + 4 + (rows0 >> 4) + g]);
           kc[g] = fmaxf(ks[g], SCALE_MIN) * p.scale2;
         }
 #pragma unroll
-        for (int g = 0; g < NG; g++) {
-          lv[g] = ks[g] > 0.f ? fmaxf(lv[g], lvref - LV_SPAN) : lvref;
-          wl[g] = ks[g] > 0.f ? ex2_ftz(lvref - lv[g]) : 0.f;
-        }
-        float Mo[2];  // O's reference
-#pragma unroll
         for (int r = 0; r < 2; r++) Mo[r] = M[r];
-        if (lvref != lvold && lvold != -INFINITY) {  // (the same in all lanes)
-          // (l lies over the eight lanes of a row: their M must move alike)
-#pragma unroll
-          for (int r = 0; r < 2; r++) {
-            float big = l[r];
-#pragma unroll
-            for (int o2 = 4; o2 < 32; o2 <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o2));
-            const float was = M[r];
-            grow_lvref(lvref - lvold, big, M[r]);
-            if (was != -INFINITY) l[r] *= exp2f(lvref - lvold - (M[r] - was));
-          }
-        }
         float al[2], e[NG][2][2];
         bool grew = false;
+        // lvref of query row r grows by d: l lies over the row's eight lanes, whose M must move alike
+        auto grow = [&](int r, float d) {
+          float big = l[r];
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
+          for (int o2 = 4; o2 < 32; o2 <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o2));
+          const float was = M[r];
+          if (d > 0.f) grow_lvref(d, big, M[r]);
+          if (was != -INFINITY) l[r] *= exp2f(d - (M[r] - was));
+        };
+        // probabilities of query row r with lv and wl of the groups
+        auto probabilities = [&](int r, const float (&lv)[NG], const float (&wl)[NG]) {
           float c[NG], mw = -INFINITY;  // largest z2 + lv
 #pragma unroll
           for (int g = 0; g < NG; g++) {
@@ -428,9 +418,46 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
             sum = fmaf(e[g][r][0] + e[g][r][1], wl[g], sum);
           }
           l[r] = fmaf(l[r], ll, sum);
-          for (uint32_t b = poison; b; b &= b - 1) {
-            const int j = j0 + __ffs(b) - 1;
-            if (j >= lo_r[r] && j < hi_r[r]) l[r] = NAN;
+        };
+        alike = alike && !edge;
+        if (alike) {
+          // every query row has seen every group so far: one lvref
+          const float was = lvref[0];
+          float ref = was, lv[NG], wl[NG];
+#pragma unroll
+          for (int g = 0; g < NG; g++) ref = fmaxf(ref, lvg[g]);
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            lv[g] = fmaxf(lvg[g], ref - LV_SPAN);
+            wl[g] = ex2_ftz(ref - lv[g]);
+          }
+          lvref[0] = lvref[1] = ref;
+          if (ref != was && was != -INFINITY) {
+#pragma unroll
+            for (int r = 0; r < 2; r++) grow(r, ref - was);
+          }
+#pragma unroll
+          for (int r = 0; r < 2; r++) probabilities(r, lv, wl);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 2; r++) {
+            const float was = lvref[r];
+            float ref = was, lv[NG], wl[NG];
+#pragma unroll
+            for (int g = 0; g < NG; g++)
+              if (!edge || (ks[g] > 0.f && j0 + g * 16 < hi_r[r] && j0 + g * 16 + 16 > lo_r[r])) ref = fmaxf(ref, lvg[g]);
+#pragma unroll
+            for (int g = 0; g < NG; g++) {
+              lv[g] = fmaxf(lvg[g], ref - LV_SPAN);
+              wl[g] = ex2_ftz(ref - lv[g]);
+            }
+            lvref[r] = ref;
+            grow(r, was == -INFINITY ? 0.f : ref - was);
+            probabilities(r, lv, wl);
+            for (uint32_t b = poison; b; b &= b - 1) {
+              const int j = j0 + __ffs(b) - 1;
+              if (j >= lo_r[r] && j < hi_r[r]) l[r] = NAN;
+            }
           }
         }
         uint32_t pb[NG][2];  // P^T fragments
@@ -479,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
       for (int o2 = 4; o2 < 32; o2 <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], o2);
       if (r0 == 0) {
         float* s3 = s_stat + (warp * 8 + 2 * t4 + r) * 3;
-        s3[0] = M[r] == -INFINITY ? -INFINITY : M[r] - P_OFF - lvref; s3[1] = M[r]; s3[2] = l[r];
+        s3[0] = M[r] == -INFINITY ? -INFINITY : M[r] - P_OFF - lvref[r]; s3[1] = M[r]; s3[2] = l[r];
       }
     }
     // O in its own reference; the readers weigh it

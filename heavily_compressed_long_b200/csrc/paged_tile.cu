@@ -59,12 +59,15 @@ constexpr int PRING = 16;      // rounds whose page parameters are kept
 constexpr uint32_t O_COL = 256;
 
 struct RoundPar {              // what the softmax needs of a round's pages (groups of 16 rows)
-  float kc[4], lv[4], wl[4];   // scale2 * k_scale, log2(v_scale), 2^(lvref - lv)
+  float kc[4], lv[4], wl[4];   // scale2 * k_scale, log2(v_scale) not below lvref - LV_SPAN, 2^(lvref - lv)
+  float lvg[4];                // log2(v_scale)
   uint32_t poison[4];          // edge rounds: rows with a NaN value, by widening warp (see look())
   uint32_t valid[2];           // rows whose page is in the cache
-  float lvref;
+  float lvref, top;            // largest log2(v_scale) from the part's first round on, of this round
   uint32_t edge;               // some query row of the item does not see the round whole
+  uint32_t pad[3];
 };
+static_assert(sizeof(RoundPar) % 16 == 0, "RoundPar");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
   return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
@@ -586,6 +589,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (h == 0) {
               RoundPar* rp = par + rg % PRING;
               if (lane < 4) {
+                rp->lvg[lane] = good ? lv : 0.f;
                 lv = fmaxf(lv, lvref - LV_SPAN);
                 rp->kc[lane] = good ? fmaxf(ks, SCALE_MIN) * p.scale2 : 0.f;
                 rp->lv[lane] = good ? lv : 0.f;
@@ -595,6 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                       ((gm >> (2 * lane)) & 1 ? 0xFFFFu : 0u) | ((gm >> (2 * lane + 1)) & 1 ? 0xFFFF0000u : 0u);
                 if (lane == 0) {
                   rp->lvref = lvref;
+                  rp->top = mx;
                   rp->edge = j0 < im.all_lo || j0 + TILE > im.all_hi || gm != 0xF;
                 }
               }
@@ -727,15 +732,32 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int q = 0; q < 4; q++) tmem_ld16(tSn + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&sv[16 * q]));
         const float4 kc4 = *reinterpret_cast<const float4*>(rp->kc), lv4 = *reinterpret_cast<const float4*>(rp->lv);
         const float4 wl4 = *reinterpret_cast<const float4*>(rp->wl);
+        float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, wl[4] = {wl4.x, wl4.y, wl4.z, wl4.w};
         const float Mo = M;           // O's reference
-        if (rp->lvref != lvref) {     // (the same for all rows)
-          if (lvref != -INFINITY) grow_lvref(rp->lvref - lvref, l, M);
-          lvref = rp->lvref;
-        }
         const uint32_t vb[2] = {range_mask(j0, lo, hi) & rp->valid[0], range_mask(j0 + 32, lo, hi) & rp->valid[1]};
+        // lvref over the groups that this query row sees: the part's, unless rounds at an edge of
+        // what the item sees left this row some of its groups out
+        float ref = lvref;
+        if (rp->edge) {
+#pragma unroll
+          for (int g = 0; g < 4; g++)
+            if (vb[g >> 1] & (g & 1 ? 0xFFFF0000u : 0xFFFFu)) ref = fmaxf(ref, rp->lvg[g]);
+        } else {
+          ref = fmaxf(ref, rp->top);
+        }
+        if (ref != rp->lvref) {
+#pragma unroll
+          for (int g = 0; g < 4; g++) {
+            lv[g] = fmaxf(rp->lvg[g], ref - LV_SPAN);
+            wl[g] = ex2_ftz(ref - lv[g]);
+          }
+        }
+        if (ref != lvref) {
+          if (lvref != -INFINITY) grow_lvref(ref - lvref, l, M);
+          lvref = ref;
+        }
         const float kc[4] = {fmaxf(kc4.x * back, SCALE_MIN), fmaxf(kc4.y * back, SCALE_MIN),
                              fmaxf(kc4.z * back, SCALE_MIN), fmaxf(kc4.w * back, SCALE_MIN)};
-        const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, wl[4] = {wl4.x, wl4.y, wl4.z, wl4.w};
         tmem_ld_wait();
         if ((vb[0] & vb[1]) != 0xFFFFFFFFu) {
 #pragma unroll

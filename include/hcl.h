@@ -419,7 +419,7 @@ HCL_API hcl_status_t hcl_paged_write(const void* k_new, int64_t k_stride, const 
  *   after; two calls that may overlap need one each.
  * Page scales must be positive and finite; those below 2^-126 count as 2^-126.  out takes each
  * row's softmax weight times its value scale in 11 bits, and where that product is below 2^-26 of
- * the query's largest, in multiples of 2^-36 of the largest (or of 2^-84 of the largest value scale
+ * the query's largest, in multiples of 2^-36 of the largest (or of 2^-59 of the largest value scale
  * that the query sees, where that is more): below 2^-37 of the largest a row may count as zero in
  * out, never in lse.  Pages outside
  * the cache, and rows beyond max_pages * page, are left out: HCL_ERR_DEVICE_FAULT.  Rows at or

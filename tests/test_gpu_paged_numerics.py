@@ -74,3 +74,58 @@ def test_attn_long_tail_over_many_blocks(hcl, orders):
         got = check_attn(hcl, dict(lens=[20000], news=[1], Hkv=1, G=G, d=64, page=64,
                                    scale=orders * float(np.log(2.0)) / 8.0), poison=poison, seed=4)
         assert_attn_lost(got, codes[0], 2.0 ** -5, G)
+
+
+# Which rows the queries see: a prompt from its start, drafts over a page's end, one token ahead of
+# the rows held, windows that have left the first pages, chunks over entries.
+VIEWS = {
+    "prompt": dict(lens=[40], news=[40], start=[0]),
+    "prompt_long": dict(lens=[300], news=[300], start=[0]),
+    "drafts": dict(lens=[18], news=[4], start=[14]),
+    "behind": dict(lens=[64], news=[1], start=[10]),
+    "window": dict(lens=[100], news=[1], W=16),
+    "window_chunk": dict(lens=[400], news=[90], W=40),
+    "entries": dict(lens=[60], news=[4], start=[100], m=4),
+}
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 64])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("view", sorted(VIEWS))
+@pytest.mark.parametrize("apart", [70, 120])
+@pytest.mark.parametrize("large", ["first", "last", "mixed"])
+def test_attn_scales_of_pages_that_a_query_does_not_see(hcl, G, shared, view, apart, large):
+    """Value scales 2^apart apart: what a query sees decides its output, though pages with far larger
+    scales stand beside it in the call."""
+    case = dict(Hkv=1, G=G, d=64, page=16, shared=shared, **VIEWS[view])
+
+    def poison(table, k, ks, v, vs, q):
+        n = -(-case["lens"][0] // 16)
+        big = {"first": np.arange(n) * 16 < (case["lens"][0] - case["news"][0]) // 16 * 16 - 16,
+               "last": np.arange(n) > 0, "mixed": np.arange(n) % 3 == 1}[large]
+        if view == "behind":
+            big = np.arange(n) > 0
+        s = ks if v is None else vs
+        for i in range(n):
+            s[table[0, i]] = 2.0 ** (20 if big[i] else 20 - apart)
+        if v is None:                       # (a key's scale is its value's: scores of ordinary size)
+            q *= 2.0 ** -22
+
+    scales = []
+
+    def keep(table, k, ks, v, vs, q):
+        poison(table, k, ks, v, vs, q)
+        scales.extend(float((ks if v is None else vs)[pg, 0]) for pg in table[0, :-(-case["lens"][0] // 16)])
+
+    got, gl, want, wl, mass, zabs = check_attn(hcl, case, poison=keep, seed=len(view))
+    # a product of weight and scale loses up to 2^-37 of the query's largest, which its mass holds for
+    # codes of ordinary size, or 2^-60 of the largest scale that it sees, for each row with codes of at most 448
+    m, W = case.get("m", 1), case.get("W", 0)
+    for i in range(case["news"][0]):
+        p = (case["start"][0] if "start" in case else case["lens"][0] - case["news"][0]) + i
+        hi = min(case["lens"][0], (p + 1) // m)
+        lo = max(0, p - W + 1) if W else 0
+        lost = 2.0 ** -60 * max(scales[lo // 16:-(-hi // 16)]) * 448 * (hi - lo)
+        diff = got[i] - want[i]
+        got[i] = np.where(np.abs(diff) <= lost, want[i], got[i] - np.clip(diff, -lost, lost))
+    assert_attn(got, gl, want, wl, mass, zabs)
