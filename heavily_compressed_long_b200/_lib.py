@@ -61,10 +61,12 @@ SIGNATURES = {
     "hcl_cp_candidates": (I, [P, I, P, I, I, I, I, P, P, P, P]),
     "hcl_cp_own": (I, [P, P, I, I, I, I, I, P, P, P]),
     "hcl_lse_merge": (I, [P, P, I, I64, I, I, P, P, P, P]),
+    "hcl_lse_merge_f32": (I, [P, P, I, I64, I, I, P, P, P, P]),
     "hcl_page_plan": (I, [P, P, I, I, P, P, I, P, I, P, I, P, P, P, P, P]),
     "hcl_paged_write": (I, [P, I64, P, I64, P, I, PKVP, P, P]),
     "hcl_paged_attn_workspace_bytes": (SZ, [I, I, I, I]),
     "hcl_paged_attn": (I, [P, I64, I, I, P, P, I, PKVP, P, I, P, I, I, I, F, P, P, P, P, SZ, P, P]),
+    "hcl_paged_attn_f32": (I, [P, I64, I, I, P, P, I, PKVP, P, I, P, I, I, I, F, P, P, P, P, SZ, P, P]),
     "hcl_selftest_bounded_wait": (I, [P, I, P]),
 }
 

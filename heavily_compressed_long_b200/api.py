@@ -17,7 +17,7 @@ from ._lib import (HCL_BF16, HCL_FP32, HCL_FP8SPLIT, HCL_MXFP4, check, hcl_kv_t,
 __all__ = ["KV", "hcl_csa_compress", "hcl_hca_compress", "hcl_quant_kv_fp8", "hcl_quant_mxfp4",
            "hcl_csa_index_scores", "hcl_csa_topk", "hcl_csa_sparse_attn", "hcl_hca_dense_attn",
            "hcl_csa_decode_step", "hcl_cache_append", "PagedKV", "hcl_page_plan", "hcl_paged_write",
-           "hcl_paged_attn", "paged_attn_workspace_bytes", "hcl_selftest_bounded_wait", "HCL_BF16",
+           "hcl_paged_attn", "hcl_paged_attn_f32", "paged_attn_workspace_bytes", "hcl_selftest_bounded_wait", "HCL_BF16",
            "HCL_FP32", "HCL_FP8SPLIT", "HCL_MXFP4"]
 
 
@@ -211,12 +211,15 @@ def hcl_cp_own(pos, gathered_idx, e0, e1, sel_out, own_out, stream=None):
 
 
 def hcl_lse_merge(o_parts, lse_parts, out, lse_out=None, sink=None, stream=None):
-    """o_parts bf16 [G, B, Tq, H, d], lse_parts fp32 [G, B, Tq, H] -> out [B, Tq, H, d]."""
+    """o_parts bf16 or fp32 [G, B, Tq, H, d], lse_parts fp32 [G, B, Tq, H] -> out bf16 [B, Tq, H, d]."""
     G = o_parts.shape[0]
     H, d = o_parts.shape[-2], o_parts.shape[-1]
     rows = lse_parts[0].numel()
-    check(lib().hcl_lse_merge(_ptr(o_parts), _ptr(lse_parts), G, rows, d, H, _ptr(sink), _ptr(out),
-                              _ptr(lse_out), _stream(stream)))
+    if o_parts.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("o_parts must be bf16 or fp32")
+    merge = lib().hcl_lse_merge_f32 if o_parts.dtype == torch.float32 else lib().hcl_lse_merge
+    check(merge(_ptr(o_parts), _ptr(lse_parts), G, rows, d, H, _ptr(sink), _ptr(out), _ptr(lse_out),
+                _stream(stream)))
 
 
 # The paged cache's calls are made once per layer and step, on small batches too, so their checks
@@ -332,6 +335,19 @@ def hcl_paged_attn(q, cu_q, q_start, store: PagedKV, table, kv_len, out, lse=Non
                    max_q=None, scale=None, sink=None, ws=None, status=None, stream=None):
     """Attention of ragged queries (bf16 [T, H, d], request b's rows cu_q[b] .. cu_q[b + 1] - 1,
     the first at position q_start[b]) over the pages that table int32 [B, max_pages] lists."""
+    return _paged_attn(lib().hcl_paged_attn, torch.bfloat16, q, cu_q, q_start, store, table, kv_len, out, lse, m, W,
+                       max_q, scale, sink, ws, status, stream)
+
+
+def hcl_paged_attn_f32(q, cu_q, q_start, store: PagedKV, table, kv_len, out, lse=None, m=1, W=0,
+                       max_q=None, scale=None, sink=None, ws=None, status=None, stream=None):
+    """hcl_paged_attn with out fp32 [T, H, d]: a part to merge with others (hcl_lse_merge)."""
+    return _paged_attn(lib().hcl_paged_attn_f32, torch.float32, q, cu_q, q_start, store, table, kv_len, out, lse, m, W,
+                       max_q, scale, sink, ws, status, stream)
+
+
+def _paged_attn(call, out_dtype, q, cu_q, q_start, store, table, kv_len, out, lse, m, W, max_q, scale, sink, ws,
+                status, stream):
     T, H, d = q.shape
     B, max_pages = table.shape
     dev = torch.cuda.current_device()
@@ -344,12 +360,12 @@ def hcl_paged_attn(q, cu_q, q_start, store: PagedKV, table, kv_len, out, lse=Non
                 ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("ws must be contiguous, on the current CUDA device")
-    check(lib().hcl_paged_attn(
+    check(call(
         qp, qs, T, H, _i32(cu_q, "cu_q", dev, B + 1), _i32(q_start, "q_start", dev, B), B,
         store.ref(dev), _i32(table, "table", dev), max_pages, _i32(kv_len, "kv_len", dev, B),
         T if max_q is None else max_q, m, W, 1.0 / math.sqrt(d) if scale is None else scale,
         None if sink is None else _dense(sink, "sink", dev, torch.float32, (H,)),
-        _dense(out, "out", dev, torch.bfloat16, q.shape),
+        _dense(out, "out", dev, out_dtype, q.shape),
         None if lse is None else _dense(lse, "lse", dev, torch.float32, (T, H)),
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
         None if status is None else _i32(status, "status", dev), _stream_on(stream, dev)))

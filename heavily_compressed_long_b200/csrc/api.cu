@@ -566,7 +566,19 @@ hcl_status_t hcl_lse_merge(const void* o_parts, const float* lse_parts, int G, i
   if (rows == 0) return HCL_OK;
   HCL_REQUIRE(o_parts && lse_parts && out, "NULL pointer");
   HCL_REQUIRE(((uintptr_t)o_parts & 3) == 0 && ((uintptr_t)out & 3) == 0, "o_parts and out must be 4-byte aligned");
-  return launch_lse_merge(o_parts, lse_parts, G, (long long)rows, d, H, sink, out, lse_out,
+  return launch_lse_merge(o_parts, false, lse_parts, G, (long long)rows, d, H, sink, out, lse_out,
+                          as_stream(stream));
+}
+
+hcl_status_t hcl_lse_merge_f32(const float* o_parts, const float* lse_parts, int G, int64_t rows, int d,
+                               int H, const float* sink, void* out, float* lse_out, void* stream) {
+  HCL_REQUIRE(G >= 1 && rows >= 0 && H >= 1, "invalid size");
+  HCL_REQUIRE(d >= 2 && d % 2 == 0 && d <= 1024, "d must be even, <= 1024");
+  if (rows == 0) return HCL_OK;
+  HCL_REQUIRE(o_parts && lse_parts && out, "NULL pointer");
+  HCL_REQUIRE(((uintptr_t)o_parts & 7) == 0 && ((uintptr_t)out & 3) == 0,
+              "o_parts must be 8-byte aligned, out 4-byte");
+  return launch_lse_merge(o_parts, true, lse_parts, G, (long long)rows, d, H, sink, out, lse_out,
                           as_stream(stream));
 }
 
@@ -638,11 +650,12 @@ size_t hcl_paged_attn_workspace_bytes(int T, int H, int Hkv, int d) {
   return hcl::paged_attn_workspace_bytes(T, H, Hkv, d);
 }
 
-hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int H, const int32_t* cu_q,
-                            const int32_t* q_start, int B, const hcl_paged_kv_t* kv,
-                            const int32_t* table, int max_pages, const int32_t* kv_len, int max_q,
-                            int m, int W, float scale, const float* sink, void* out, float* lse,
-                            void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+// out: bf16, or fp32
+static hcl_status_t paged_attn(const void* q, int64_t q_stride, int T, int H, const int32_t* cu_q,
+                               const int32_t* q_start, int B, const hcl_paged_kv_t* kv,
+                               const int32_t* table, int max_pages, const int32_t* kv_len, int max_q,
+                               int m, int W, float scale, const float* sink, void* out, bool f32, float* lse,
+                               void* ws, size_t ws_bytes, int32_t* status, void* stream) {
   HCL_REQUIRE(T >= 0 && B >= 0, "negative size");
   hcl_status_t e = check_paged(kv);
   if (e != HCL_OK) return e;
@@ -665,8 +678,26 @@ hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int H, const
   HCL_REQUIRE(ws_bytes >= need && (need == 0 || (ws && aligned16(ws))),
               "workspace too small or not 16-byte aligned: need %zu bytes", need);
   PagedAttnArgs a{q, q_stride, T, H, cu_q, q_start, B, *kv, table, max_pages, kv_len, max_q, m, W,
-                  scale, sink, out, lse, status};
+                  scale, sink, out, f32 ? static_cast<float*>(out) : nullptr, lse, status};
   return launch_paged_attn(a, ws, as_stream(stream));
+}
+
+hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int H, const int32_t* cu_q,
+                            const int32_t* q_start, int B, const hcl_paged_kv_t* kv,
+                            const int32_t* table, int max_pages, const int32_t* kv_len, int max_q,
+                            int m, int W, float scale, const float* sink, void* out, float* lse,
+                            void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  return paged_attn(q, q_stride, T, H, cu_q, q_start, B, kv, table, max_pages, kv_len, max_q, m, W, scale,
+                    sink, out, false, lse, ws, ws_bytes, status, stream);
+}
+
+hcl_status_t hcl_paged_attn_f32(const void* q, int64_t q_stride, int T, int H, const int32_t* cu_q,
+                                const int32_t* q_start, int B, const hcl_paged_kv_t* kv,
+                                const int32_t* table, int max_pages, const int32_t* kv_len, int max_q,
+                                int m, int W, float scale, const float* sink, float* out, float* lse,
+                                void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  return paged_attn(q, q_stride, T, H, cu_q, q_start, B, kv, table, max_pages, kv_len, max_q, m, W, scale,
+                    sink, out, true, lse, ws, ws_bytes, status, stream);
 }
 
 hcl_status_t hcl_selftest_bounded_wait(int32_t* status, int limit_us, void* stream) {

@@ -93,10 +93,16 @@ __global__ void cp_own_kernel(const int32_t* __restrict__ pos, const int32_t* __
   for (int j = cnt[1] + threadIdx.x; j < k; j += blockDim.x) oo[j] = -1;
 }
 
-// One warp per (row = sequence x head): G partials o [G, rows, d] bf16, lse [G, rows] fp32
+// One warp per (row = sequence x head): G partials o [G, rows, d] bf16 or fp32, lse [G, rows] fp32
 // (natural log) -> out [rows, d] bf16, lse_out [rows].
 // A NaN lse (a NaN among the part's queries or rows) has no order: it makes the row NaN.
-__global__ void lse_merge_kernel(const __nv_bfloat16* o, const float* lse, int G, long long rows, int d, int H,
+__device__ __forceinline__ float2 part_pair(const __nv_bfloat16* p) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ float2 part_pair(const float* p) { return *reinterpret_cast<const float2*>(p); }
+
+template <typename T>
+__global__ void lse_merge_kernel(const T* o, const float* lse, int G, long long rows, int d, int H,
                                  const float* sink, __nv_bfloat16* out, float* lse_out) {
   pdl_enter();
   const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -119,9 +125,9 @@ __global__ void lse_merge_kernel(const __nv_bfloat16* o, const float* lse, int G
       const float l = lse[g * rows + r];
       if (l == -INFINITY) continue;
       const float wgt = __expf(l - M);
-      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(o + ((size_t)g * rows + r) * d + c);
-      a0 = fmaf(wgt, __bfloat162float(v.x), a0);
-      a1 = fmaf(wgt, __bfloat162float(v.y), a1);
+      const float2 v = part_pair(o + ((size_t)g * rows + r) * d + c);
+      a0 = fmaf(wgt, v.x, a0);
+      a1 = fmaf(wgt, v.y, a1);
     }
     *reinterpret_cast<__nv_bfloat162*>(out + (size_t)r * d + c) = __floats2bfloat162_rn(a0 * inv, a1 * inv);
   }
@@ -149,13 +155,15 @@ hcl_status_t launch_cp_own(const int32_t* pos, const int32_t* gidx, int B, int n
                     "cp own launch");
 }
 
-hcl_status_t launch_lse_merge(const void* o, const float* lse, int G, long long rows, int d, int H,
+hcl_status_t launch_lse_merge(const void* o, bool f32, const float* lse, int G, long long rows, int d, int H,
                               const float* sink, void* out, float* lse_out, cudaStream_t st) {
   if (rows == 0) return HCL_OK;
-  const long long threads = rows * 32;
-  return check_cuda(launch_pdl(lse_merge_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256),
-                               0, st, 1, static_cast<const __nv_bfloat16*>(o), lse, G, rows, d, H,
-                               sink, static_cast<__nv_bfloat16*>(out), lse_out),
+  const dim3 grid((unsigned)((rows * 32 + 255) / 256)), block(256);
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(out);
+  return check_cuda(f32 ? launch_pdl(lse_merge_kernel<float>, grid, block, 0, st, 1, static_cast<const float*>(o), lse,
+                                     G, rows, d, H, sink, to, lse_out)
+                        : launch_pdl(lse_merge_kernel<__nv_bfloat16>, grid, block, 0, st, 1,
+                                     static_cast<const __nv_bfloat16*>(o), lse, G, rows, d, H, sink, to, lse_out),
                     "lse merge launch");
 }
 

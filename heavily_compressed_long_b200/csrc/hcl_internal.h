@@ -187,7 +187,8 @@ hcl_status_t launch_cp_candidates(const void* scores, int score_fmt, const int32
                                   int32_t* status, cudaStream_t st);
 hcl_status_t launch_cp_own(const int32_t* pos, const int32_t* gidx, int B, int n, int k, int e0,
                            int e1, int32_t* sel_out, int32_t* own_out, cudaStream_t st);
-hcl_status_t launch_lse_merge(const void* o, const float* lse, int G, long long rows, int d, int H,
+// o: bf16, or fp32
+hcl_status_t launch_lse_merge(const void* o, bool f32, const float* lse, int G, long long rows, int d, int H,
                               const float* sink, void* out, float* lse_out, cudaStream_t st);
 
 // Fixed device scratch of hcl_csa_sparse_attn_noalloc (split-KV partials), and its device
@@ -238,7 +239,8 @@ struct PagedAttnArgs {
   int max_q, m, W;
   float scale;
   const float* sink;
-  void* out;
+  void* out;     // bf16,
+  float* out32;  // or fp32 where it is given
   float* lse;
   int32_t* status;
 };

@@ -76,8 +76,13 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
       for (int k = 0; k < n; k++) add_part<E>(a, part(k) + ROWS * 4 + (size_t)row * D + lane * E, __shfl_sync(~0u, f, k));
       const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &lse);
 #pragma unroll
-      for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(out + lane * E + e) = fo == 0.f ? 0u : bf16x2_of(a[e] * fo, a[e + 1] * fo);
+      for (int e = 0; e < E; e += 2) {
+        const float2 x = fo == 0.f ? make_float2(0.f, 0.f) : make_float2(a[e] * fo, a[e + 1] * fo);
+        if (p.a.out32)
+          *reinterpret_cast<float2*>(p.a.out32 + orow * D + lane * E + e) = x;
+        else
+          *reinterpret_cast<uint32_t*>(out + lane * E + e) = bf16x2_of(x.x, x.y);
+      }
       if (lane == 0 && p.a.lse) p.a.lse[orow] = lse;
       continue;
     }
@@ -120,7 +125,11 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
       float x = 0.f;
 #pragma unroll
       for (int v = 0; v < MW; v++) x += s_o[v][e];
-      out[e] = __float2bfloat16(fo == 0.f ? 0.f : x * fo);
+      x = fo == 0.f ? 0.f : x * fo;
+      if (p.a.out32)
+        p.a.out32[orow * D + e] = x;
+      else
+        out[e] = __float2bfloat16(x);
     }
     if (tid == 0 && p.a.lse) p.a.lse[orow] = lse;
     __syncthreads();

@@ -559,8 +559,12 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
           const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
           float lse;
           const float f = finish_row<true>(mt, Mt, lt, p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + col) =
-              f == 0.f ? make_uint2(0, 0) : make_uint2(bf16x2_of(a.x * f, a.y * f), bf16x2_of(a.z * f, a.w * f));
+          a = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+          if (p.a.out32)
+            *reinterpret_cast<float4*>(p.a.out32 + orow * D + col) = a;
+          else
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + orow * D + col) =
+                make_uint2(bf16x2_of(a.x, a.y), bf16x2_of(a.z, a.w));
           if (col == 0 && p.a.lse) p.a.lse[orow] = lse;
         } else {
           *reinterpret_cast<float4*>(pp + ROWS_SMALL * 4 + row * D + col) = a;

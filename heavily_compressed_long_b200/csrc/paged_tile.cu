@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 32; j++)
             if (fb != 0.f) x[j] = fmaf(__uint_as_float(y[j]), fb, x[j]);
         }
-        if (whole) {
+        if (whole && !p.a.out32) {
           // bf16, 64 dimensions in the rows' 128 bytes: 8 pieces, four of them now
           const int half = (c >> 3) & 4;
 #pragma unroll
@@ -936,8 +936,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int k = 0; k < 8; k++) {
             const int r = 4 * k + r_in;
             const float4 v = *reinterpret_cast<const float4*>(stage + r * 128 + ((e_in ^ (r & 7)) << 4));
+            const int to = __shfl_sync(~0u, orow, r);
             if (irow0 + r < rows)
-              *reinterpret_cast<float4*>(pp + ITEM * 4 + (size_t)(irow0 + r) * D + c + e_in * 4) = v;
+              *reinterpret_cast<float4*>((whole ? p.a.out32 + (size_t)to * D : pp + ITEM * 4 + (size_t)(irow0 + r) * D) + c +
+                                         e_in * 4) = v;
           }
         }
         __syncwarp();

@@ -233,13 +233,14 @@ class PagedAttnLayer:
                             stream=stream)
 
     def attend(self, q, out, lse=None, max_q=None, cu_q=None, q_start=None, sink=None, stream=None):
-        """q bf16 [T, H, d]: the plan's new rows, unless cu_q and q_start say otherwise."""
+        """q bf16 [T, H, d]: the plan's new rows, unless cu_q and q_start say otherwise.  out bf16, or
+        fp32 (a part that hcl_lse_merge joins with others)."""
         b = self.batch
-        return api.hcl_paged_attn(q, b.cu_new if cu_q is None else cu_q,
-                                  b.start if q_start is None else q_start, self.store, b.table,
-                                  b.seq_len, out, lse=lse, m=self.m, W=self.W, max_q=max_q,
-                                  sink=self.sink if sink is None else sink, ws=self.ws,
-                                  status=b.status, stream=stream)
+        attn = api.hcl_paged_attn_f32 if out.dtype == torch.float32 else api.hcl_paged_attn
+        return attn(q, b.cu_new if cu_q is None else cu_q, b.start if q_start is None else q_start,
+                    self.store, b.table, b.seq_len, out, lse=lse, m=self.m, W=self.W, max_q=max_q,
+                    sink=self.sink if sink is None else sink, ws=self.ws, status=b.status,
+                    stream=stream)
 
     def step(self, q, k_new, v_new, out, lse=None, max_q=None, stream=None):
         self.write(k_new, v_new, stream=stream)
@@ -262,7 +263,8 @@ class PagedHcaLayer:
         # (its queries are the raw batch's)
         self.entry_layer = PagedAttnLayer(entries, n_entry_pages, H, 1, d, shared=True, m=mh,
                                           device=device, max_T=raw.T)
-        self.o_parts = torch.zeros(2, raw.T, H, d, dtype=torch.bfloat16, device=device)
+        # (fp32: the parts may cancel, and out is rounded once)
+        self.o_parts = torch.zeros(2, raw.T, H, d, dtype=torch.float32, device=device)
         self.lse_parts = torch.empty(2, raw.T, H, dtype=torch.float32, device=device)
 
     def attend(self, q, out, lse=None, max_q=None, stream=None):

@@ -325,6 +325,10 @@ HCL_API hcl_status_t hcl_cp_own(const int32_t* pos, const int32_t* gathered_idx,
 HCL_API hcl_status_t hcl_lse_merge(const void* o_parts, const float* lse_parts, int G, int64_t rows,
                                    int d, int H, const float* sink, void* out, float* lse_out,
                                    void* stream);
+/* The same on fp32 parts (o_parts fp32 [G, rows, d], 8-byte aligned): out is rounded once. */
+HCL_API hcl_status_t hcl_lse_merge_f32(const float* o_parts, const float* lse_parts, int G,
+                                       int64_t rows, int d, int H, const float* sink, void* out,
+                                       float* lse_out, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * Paged 8-bit KV cache for ragged batches [Yanbaoke §5 KV cache management names a paged,
@@ -437,6 +441,14 @@ HCL_API hcl_status_t hcl_paged_attn(const void* q, int64_t q_stride, int T, int 
                                     const int32_t* kv_len, int max_q, int m, int W, float scale,
                                     const float* sink, void* out, float* lse, void* ws,
                                     size_t ws_bytes, int32_t* status, void* stream);
+/* The same with out fp32 [T, H, d]: a part that hcl_lse_merge_f32 joins with others. */
+HCL_API hcl_status_t hcl_paged_attn_f32(const void* q, int64_t q_stride, int T, int H,
+                                        const int32_t* cu_q, const int32_t* q_start, int B,
+                                        const hcl_paged_kv_t* kv, const int32_t* table,
+                                        int max_pages, const int32_t* kv_len, int max_q, int m,
+                                        int W, float scale, const float* sink, float* out,
+                                        float* lse, void* ws, size_t ws_bytes, int32_t* status,
+                                        void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * Failure-detection self-test: launches one block whose bounded wait on an mbarrier that

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from tests import paged_ref as ref
-from tests.test_gpu_paged import PlanState, i32, status
+from tests.test_gpu_paged import PlanState, assert_attn, held_rows, i32, make_cache, status
 
 pytestmark = pytest.mark.gpu
 
@@ -196,3 +196,64 @@ def test_hca_layer_with_more_queries_than_new_entries(hcl, H, T, entries_T):
         got.append(layer.attend(q, torch.zeros(T, H, 128, dtype=torch.bfloat16, device=DEV), max_q=T))
         assert raw.status.item() == 0 and ent.status.item() == 0
     assert torch.isfinite(got[0]).all() and (got[0] != 0).any() and torch.equal(*got)
+
+
+@pytest.mark.parametrize("H,T,n_entries,raw_rows", [(16, 4, 8, 200), (64, 40, 0, 200), (16, 40, 8, 203), (4, 1, 24, 70)])
+@pytest.mark.parametrize("with_sink", [False, True])
+def test_hca_layer_rounds_once(hcl, H, T, n_entries, raw_rows, with_sink):
+    """The layer against one softmax over entries, window and sink in 64 bits, at the bound of the
+    attention itself: the parts are not rounded before they are merged."""
+    gen = torch.Generator().manual_seed(H + T)
+    sink = torch.randn(H, generator=gen) if with_sink else None
+    layer, raw, ent = hca_layer(H, T, 8, n_entries, gen, sink=None if sink is None else sink.cuda(), raw_rows=raw_rows)
+    for _ in range(12):
+        q = (torch.randn(T, H, 128, generator=gen) * 0.3).to(torch.bfloat16)
+        out = torch.zeros(T, H, 128, dtype=torch.bfloat16, device=DEV)
+        lse = torch.zeros(T, H, device=DEV)
+        layer.attend(q.cuda(), out, lse=lse, max_q=T)
+        new, start = int(raw.cu_new[1]), int(raw.start[0])
+        rows = [held_rows(b, x, 0)[0][:, 0] for b, x in ((ent, layer.entry_layer), (raw, layer.raw_layer))]
+        want, mass = np.zeros((new, H, 128)), np.zeros((new, H, 128))
+        wl, zabs = np.zeros((new, H)), np.zeros((new, H))
+        for i in range(new):
+            p = start + i
+            x = np.concatenate([rows[0][:(p + 1) // 16], rows[1][max(0, p - 63):p + 1]])
+            z = ref.f64(q[i]) @ x.T / math.sqrt(128)
+            zz = z if sink is None else np.concatenate([z, ref.f64(sink)[:, None]], 1)
+            wl[i] = np.log(np.exp(zz - zz.max(1, keepdims=True)).sum(1)) + zz.max(1)
+            w = np.exp(z - wl[i][:, None])
+            want[i], mass[i] = w @ x, w @ np.abs(x)
+            zabs[i] = (np.abs(ref.f64(q[i])) @ np.abs(x).T).max(1) / math.sqrt(128)
+        assert_attn(ref.f64(out)[:new], ref.f64(lse)[:new], want, wl, mass, zabs)
+
+
+# ------------------------------------------------------------------------------------ parts in fp32
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,lens,news", [(8, [1, 65, 300], [1, 1, 1]), (16, [40, 9], [1, 0]), (8, [30000], [1]),
+                                         (8, [3000] * 40, [1] * 40), (128, [100, 5], [1, 1]), (64, [30000, 70], [1, 2]),
+                                         (8, [200, 90], [200, 33]), (16, [9000], [300])])
+def test_attn_fp32_out(hcl, d, G, lens, news):
+    """The fp32 output rounds to the bf16 one, whichever kernel and merge writes it; rows behind the
+    last request stay."""
+    gen = torch.Generator().manual_seed(G)
+    table, k, ks, v, vs = make_cache(lens, 32, 2, d, False, gen)
+    T, H = sum(news) + 2, 2 * G
+    q = torch.randn(T, H, d, generator=gen).to(torch.bfloat16).cuda()
+    store = hcl.PagedKV(k.cuda(), ks.cuda(), v.cuda(), vs.cuda())
+    args = (q, i32(np.concatenate([[0], np.cumsum(news)])), i32([a - b for a, b in zip(lens, news)]), store, i32(table),
+            i32(lens))
+    res = []
+    for call, dtype in ((hcl.hcl_paged_attn, torch.bfloat16), (hcl.hcl_paged_attn_f32, torch.float32)):
+        out, lse = torch.full((T, H, d), 7.0, dtype=dtype, device=DEV), torch.full((T, H), 7.0, device=DEV)
+        call(*args, out, lse=lse, max_q=max(news))
+        res.append((out, lse))
+    (a, al), (b, bl) = res
+    assert torch.equal(a, b.to(torch.bfloat16)) and torch.equal(al, bl)
+    assert bool((b[-2:] == 7.0).all()) and torch.isfinite(b).all()
+    assert not torch.equal(b[:-2], a[:-2].float())
+    with pytest.raises(ValueError):
+        hcl.hcl_paged_attn_f32(*args, torch.empty(T, H, d, dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError):
+        hcl.hcl_lse_merge(torch.empty(1, 1, T, H, d, dtype=torch.float16, device=DEV), al[None, None], a[None])
