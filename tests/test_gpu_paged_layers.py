@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from tests import paged_ref as ref
-from tests.test_gpu_paged import PlanState, assert_attn, held_rows, i32, make_cache, status
+from tests.test_gpu_paged import PlanState, assert_attn, check_attn, held_rows, i32, make_cache, status
 
 pytestmark = pytest.mark.gpu
 
@@ -257,3 +257,67 @@ def test_attn_fp32_out(hcl, d, G, lens, news):
         hcl.hcl_paged_attn_f32(*args, torch.empty(T, H, d, dtype=torch.bfloat16, device=DEV))
     with pytest.raises(ValueError):
         hcl.hcl_lse_merge(torch.empty(1, 1, T, H, d, dtype=torch.float16, device=DEV), al[None, None], a[None])
+
+
+# ------------------------------------------------------------------------------------ calls together
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_attn_calls_on_streams(hcl, graph):
+    """Calls in flight on several streams, each with its own workspace, whose long requests are split
+    over blocks: finite, the bits of a call alone, and sampled rows against 64 bits; also captured,
+    the graphs replayed side by side."""
+    gen = torch.Generator().manual_seed(12)
+    calls = []
+    for lens, news, G, d in (([4000, 70, 900], [300, 1, 64], 8, 128), ([3000, 2500, 10], [1, 1, 1], 64, 64),
+                             ([9000, 30, 700], [1, 1, 1], 8, 128), ([6000, 500], [40, 300], 16, 64)):
+        table, k, ks, v, vs = make_cache(lens, 32, 2, d, False, gen)
+        T = sum(news)
+        q = torch.randn(T, 2 * G, d, generator=gen).to(torch.bfloat16)
+        cu, start = np.concatenate([[0], np.cumsum(news)]), [a - b for a, b in zip(lens, news)]
+        args = (q.cuda(), i32(cu), i32(start), hcl.PagedKV(k.cuda(), ks.cuda(), v.cuda(), vs.cuda()), i32(table), i32(lens))
+        ws = torch.empty(hcl.paged_attn_workspace_bytes(T, 2 * G, 2, d), dtype=torch.uint8, device=DEV)
+        out, lse = torch.empty(T, 2 * G, d, dtype=torch.bfloat16, device=DEV), torch.empty(T, 2 * G, device=DEV)
+        alone = hcl.hcl_paged_attn(*args, torch.empty_like(out), max_q=max(news), ws=ws)
+        torch.cuda.synchronize()
+        calls.append((args, ws, max(news), out, lse, torch.cuda.Stream(), alone, (lens, news, start, cu, table, k, ks, v, vs, q)))
+    graphs = []
+    for args, ws, mq, out, lse, stream, _, _ in calls:
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                hcl.hcl_paged_attn(*args, out, lse=lse, max_q=mq, ws=ws, stream=stream)
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (args, ws, mq, out, lse, stream, _, _) in enumerate(calls):
+            if graph:
+                with torch.cuda.stream(stream):
+                    graphs[i].replay()
+            else:
+                hcl.hcl_paged_attn(*args, out, lse=lse, max_q=mq, ws=ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, _, _, out, lse, _, alone, (lens, news, start, cu, table, k, ks, v, vs, q) in calls:
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all() and torch.equal(out, alone)
+        H, d = q.shape[1], q.shape[2]
+        for b in range(len(lens)):
+            for i in {0, news[b] // 2, news[b] - 1}:
+                for h in (0, H // 2 - 1, H - 1):
+                    g, t = h // (H // 2), int(cu[b]) + i
+                    w = ref.attn(ref.f64(q[t:t + 1, h:h + 1]), [0, 1], [start[b] + i], lens[b:b + 1], table[b:b + 1],
+                                 k[:, g:g + 1].numpy(), ks[:, g:g + 1].numpy(), v[:, g:g + 1].numpy(),
+                                 vs[:, g:g + 1].numpy(), 32, 1, 0, 1 / math.sqrt(d))
+                    assert_attn(ref.f64(out[t:t + 1, h:h + 1]), ref.f64(lse[t:t + 1, h:h + 1]), *w)
+
+
+@pytest.mark.parametrize("d,W,m", [(64, 0, 1), (128, 20, 1), (64, 0, 4), (64, 0, 2 ** 31 - 1)])
+def test_attn_most_requests(hcl, d, W, m):
+    """8192 requests in one call, decode among short chunks, some without queries or rows."""
+    gen = torch.Generator().manual_seed(2)
+    rng = np.random.default_rng(2)
+    B = 8192
+    lens = rng.integers(0, 40, B).tolist()
+    news = [min(int(n), 1 + l) for n, l in zip(rng.choice([0, 1, 1, 1, 1, 1, 2, 9], B), lens)]
+    case = dict(lens=lens, news=news, Hkv=1, G=4, d=d, page=16, shared=True, W=W, m=m, sink=W == 0,
+                start=[min(2 ** 31 - 20, max(0, l * m - n)) for l, n in zip(lens, news)])
+    assert_attn(*check_attn(hcl, case))
