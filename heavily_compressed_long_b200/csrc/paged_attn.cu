@@ -28,6 +28,9 @@ __device__ __forceinline__ void add_part(float (&a)[E], const float* src, float 
 }
 
 constexpr int MW = 8;
+// Parts that a warp of its own joins: a lane holds each one's statistics.  (The whole block a row
+// for every item: drafts 82 -> 103 us, window chunks 54 -> 81, prompts 585 -> 676, grouped decode
+// 246 -> 250.)
 constexpr int FEW = 32;
 template <int D, int ROWS>
 __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
