@@ -7,8 +7,8 @@
 // asynchronous copies that complete on the same mbarrier; page ids are read eight units at a time,
 // eight ahead.  With at most 8 query rows consumer warps 0, 1 take the even units and 2, 3 the odd
 // ones, each 32 rows; with 9 to 16 every unit goes to all four, warps 0, 1 with the first 8 query
-// rows and 2, 3 with the others (decode over 64 entries, 16 heads: 13 us with each half on a unit
-// of its own, 10.9 so).
+// rows and 2, 3 with the others, so that every code is converted in two warps (device time of
+// 4 requests on up to 512 entries, 16 heads: 13 us with each half on a unit of its own, 10.6 so).
 // Each has its own running softmax, so warps never wait for one another inside an item:
 //   S^T (16 KV rows x 8 query rows) by m16n8k16 fp16 MMAs: KV rows are the M of the MMA, so up to
 //   8 query rows (a group of 8 heads) waste none of it.  The K fragments come from ldmatrix on
@@ -19,7 +19,9 @@
 //   (movmatrix).
 // The bytes bound the kernel once the chain from load to store is covered.  32 requests of up to
 // 32 K rows, 8 KV heads of 8 query heads (1.37 GB, 209 us at the copy rate): 300 us with query
-// rows as M, 16 KV rows a warp and step; 265 us with 32 KV rows; 218 us in this form.
+// rows as M, 16 KV rows a warp and step; 265 us with 32 KV rows; 222 us in this form (device
+// time).  A lvref for each query row costs 2.5 % of that though it is one number while all rows
+// have seen all groups; formed for each row in every step it cost 7 %.
 #include <algorithm>
 
 #include "paged_common.cuh"

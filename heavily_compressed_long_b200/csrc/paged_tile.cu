@@ -36,8 +36,8 @@
 // between the groups (prompts 589 -> 710), scores read twice in rolled halves (chunk 1285), rings
 // of 4 or 2 tiles, two or four staging units (the same within 1 %).  Code that runs once an item
 // is kept in loops: unrolled it waited for instructions (prompts 622 -> 588 us).
-//   decode, 8 x 128 K rows x 128 heads on one KV head: 75 us (27 at the MMA rate)
-//   chunk of 2048 x 16 heads on 65536 rows: 1148 us (653);  prompts, 4 x 4096 x 32 heads: 579 us (206)
+//   decode, 8 x 128 K rows x 128 heads on one KV head: 77 us (27 at the MMA rate)
+//   chunk of 2048 x 16 heads on 65536 rows: 1160 us (653);  prompts, 4 x 4096 x 32 heads: 585 us (206)
 #include <algorithm>
 
 #include "paged_common.cuh"
