@@ -11,7 +11,8 @@
 //
 // Numerics.  Codes are exact in fp16 and so is a query row after its exponent is taken out
 // (2^e with the row's largest magnitude in [2^14, 2^15); components below 2^-28 of the largest
-// lose bits, by at most 2^-40 of it), so the fp16 products of Q K^T are exact and summed in fp32:  z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
+// lose bits, by at most 2^-40 of it), so the fp16 products of Q K^T are exact and summed in fp32:
+// z2 = log2(e) * scale * q.k = S * kc * 2^e,  kc = scale2 * k_scale.
 // A value page's scale goes into the exponent of the probabilities: P = 2^(z2 + lv - M + P_OFF)
 // with lv = log2(v_scale) and M >= max(z2 + lv) - (15 - P_OFF) a running reference, rounded to
 // fp16, and O = sum P * code in fp32 needs no further scale.  fp16 holds 11 bits down to 2^-14 and
@@ -236,15 +237,6 @@ __device__ __forceinline__ uint32_t half2_of_codes(uint16_t c) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
-}
-// The same as bf16 (exact).
-__device__ __forceinline__ uint32_t bf2_of_codes(uint16_t c) {
-  const uint32_t h = half2_of_codes(c);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return bf16x2_of(f.x, f.y);
-}
-__device__ __forceinline__ unsigned long long f2_sub(unsigned long long a, unsigned long long b) {
-  return f2_fma(b, f2_make(-1.f, -1.f), a);
 }
 // 0xFF in every byte of x that is a NaN code (0x7F with either sign).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {

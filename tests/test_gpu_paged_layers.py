@@ -19,7 +19,7 @@ DEV = "cuda"
 # ------------------------------------------------------------------------------------ plan
 
 
-@pytest.mark.parametrize("B", [3040, 3046, 3047, 3060, 3071, 3072, 8192])
+@pytest.mark.parametrize("B", [3040, 3046, 3047, 3060, 3071, 3080, 8192])
 def test_plan_many_requests(hcl, B):
     """Numbers of requests around the shared memory that a launch has without asking, and the most."""
     rng = np.random.default_rng(B)
