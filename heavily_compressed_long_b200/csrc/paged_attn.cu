@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
     const size_t orow = (size_t)(r.c0 + qi) * p.a.H + head;
     const float sink2 = p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + orow * D;
-    float m = -INFINITY, M = -INFINITY, l = 0.f, lse;
+    float m = -INFINITY, M = -INFINITY, l = 0.f, f2, lse;
     if (few) {
       float4 h = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
       if (lane < n) h = *reinterpret_cast<const float4*>(part(lane) + row * 4);
@@ -77,10 +77,10 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
       for (int e = 0; e < E; e++) a[e] = 0.f;
 #pragma unroll 4
       for (int k = 0; k < n; k++) add_part<E>(a, part(k) + ROWS * 4 + (size_t)row * D + lane * E, __shfl_sync(~0u, f, k));
-      const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &lse);
+      const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &f2, &lse);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const float2 x = fo == 0.f ? make_float2(0.f, 0.f) : make_float2(a[e] * fo, a[e + 1] * fo);
+        const float2 x = fo == 0.f ? make_float2(0.f, 0.f) : make_float2(a[e] * fo * f2, a[e + 1] * fo * f2);
         if (p.a.out32)
           *reinterpret_cast<float2*>(p.a.out32 + orow * D + lane * E + e) = x;
         else
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(MW * 32) paged_merge_kernel(const Params p) {
 #pragma unroll
     for (int e = 0; e < E; e++) s_o[warp][lane * E + e] = a[e];
     __syncthreads();
-    const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &lse);
+    const float fo = finish_row<ROWS == ROWS_SMALL>(m, M, l, sink2, &f2, &lse);
     for (int e = tid; e < D; e += MW * 32) {
       float x = 0.f;
 #pragma unroll
       for (int v = 0; v < MW; v++) x += s_o[v][e];
-      x = fo == 0.f ? 0.f : x * fo;
+      x = fo == 0.f ? 0.f : x * fo * f2;
       if (p.a.out32)
         p.a.out32[orow * D + e] = x;
       else

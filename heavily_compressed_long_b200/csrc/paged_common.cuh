@@ -251,10 +251,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
       : "memory");
 }
 
-// The final row from O (value units), l and m (log2 units): factor for O and the log-sum-exp.
+// The final row from O (value units), l and m (log2 units): a factor for O, a second one for the
+// product (both at once may be below fp32's numbers: 2^lvref over a sum of 2^P_OFF each) and the
+// log-sum-exp.
 // M: O's reference; the sink's logit in log2 units, or -inf.
 template <bool ROWS>
-__device__ __forceinline__ float finish_row(float m, float M, float l, float sink2, float* lse) {
+__device__ __forceinline__ float finish_row(float m, float M, float l, float sink2, float* second, float* lse) {
+  *second = 0.f;
   if (!(l > 0.f) && !(l != l)) {  // no row
     *lse = sink2 == -INFINITY ? -INFINITY : sink2 * LN2;
     return 0.f;
@@ -262,7 +265,8 @@ __device__ __forceinline__ float finish_row(float m, float M, float l, float sin
   const float mm = fmaxf(m, sink2);
   const float lt = l * exp2f(m - mm) + (sink2 == -INFINITY ? 0.f : exp2f(sink2 - mm));
   *lse = (mm + log2f(lt)) * LN2;
-  return exp2f(M - (ROWS ? P_OFF_ROWS : P_OFF_TILE) - mm) / lt;
+  *second = exp2f(M - (ROWS ? P_OFF_ROWS : P_OFF_TILE) - mm);
+  return 1.f / lt;
 }
 
 // Kernels for requests of up to ROWS_SMALL query rows (`rows`: the most that one of them can

@@ -559,9 +559,10 @@ __global__ void __launch_bounds__(THREADS, (Cfg<D, SHARED, RH>::BLOCKS))
         if (whole) {
           const int i = p.by_G.div(row), head = w.g * p.G + row - i * p.G;
           const size_t orow = (size_t)(w.r.c0 + i) * p.a.H + head;
-          float lse;
-          const float f = finish_row<true>(mt, Mt, lt, p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
-          a = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+          float lse, f2;
+          const float f = finish_row<true>(mt, Mt, lt, p.a.sink ? p.a.sink[head] * LOG2E : -INFINITY, &f2, &lse);
+          a = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                       : make_float4(a.x * f * f2, a.y * f * f2, a.z * f * f2, a.w * f * f2);
           if (p.a.out32)
             *reinterpret_cast<float4*>(p.a.out32 + orow * D + col) = a;
           else

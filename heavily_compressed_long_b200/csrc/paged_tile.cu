@@ -853,7 +853,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // Single mode: the groups join their results, each reading both O's (the same lanes of TMEM)
       // for its half of the dimensions.
-      float fa = 1.f, fb = 0.f;  // factors of the (first) O and the other group's
+      float fa = 1.f, fb = 0.f;  // factors of the (first) O and the other group's,
+      float f2 = 1.f;            // and of their sum
       if (!pair) {
         *reinterpret_cast<float4*>(s_stat + (t * 128 + row) * 4) = make_float4(m, M, l, 0.f);
         tc_fence_before();
@@ -872,7 +873,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       float* pp = p.part + (2 * (size_t)blockIdx.x + (im->head ? 0 : 1)) * part_floats(ITEM, D);
       if (whole) {
         float lse;
-        const float f = finish_row<false>(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &lse);
+        const float f = finish_row<false>(m, M, l, p.a.sink && valid ? p.a.sink[head] * LOG2E : -INFINITY, &f2, &lse);
         fa *= f;
         fb *= f;
         if (valid && p.a.lse && (pair || t == 0)) p.a.lse[orow] = lse;
@@ -904,6 +905,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 32; j++)
             if (fb != 0.f) x[j] = fmaf(__uint_as_float(y[j]), fb, x[j]);
         }
+#pragma unroll
+        for (int j = 0; j < 32; j++) x[j] *= f2;
         if (whole && !p.a.out32) {
           // bf16, 64 dimensions in the rows' 128 bytes: 8 pieces, four of them now
           const int half = (c >> 3) & 4;

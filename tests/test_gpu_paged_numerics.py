@@ -129,3 +129,18 @@ def test_attn_scales_of_pages_that_a_query_does_not_see(hcl, G, shared, view, ap
         diff = got[i] - want[i]
         got[i] = np.where(np.abs(diff) <= lost, want[i], got[i] - np.clip(diff, -lost, lost))
     assert_attn(got, gl, want, wl, mass, zabs)
+
+
+@pytest.mark.parametrize("G,lens,news", [(8, [40, 3000], [1, 1]), (16, [200000], [1]), (128, [700], [1]), (64, [200000], [1]),
+                                         (8, [90], [60]), (4, [3000, 5], [3, 3])])
+@pytest.mark.parametrize("scale", [-126, -118, 119])
+def test_attn_smallest_and_largest_value_scales(hcl, G, lens, news, scale):
+    """Values of 2^-126 (and up to 2^119) times their codes come out with bf16's precision however
+    long the sum of the weights."""
+    def poison(table, k, ks, v, vs, q):
+        vs[:] = 2.0 ** scale
+        ks[:] = 2.0 ** -7
+        v &= 0x7F
+
+    got, gl, want, wl, mass, zabs = check_attn(hcl, dict(lens=lens, news=news, Hkv=1, G=G, d=64, page=64, qs=0.2), poison=poison)
+    assert_attn(got * 2.0 ** -scale, gl, want * 2.0 ** -scale, wl, mass * 2.0 ** -scale, zabs)
